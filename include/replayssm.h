@@ -310,6 +310,135 @@ int replayssm_recurrent_verify(const rssm_desc *desc, float *pool, const int32_t
 int replayssm_recurrent_accept(const rssm_desc *desc, int32_t *sel,
                                const int32_t *n_keep, int32_t T, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Mixer operators: what stands around the recurrence in an SSM layer.  The
+ * rows of the layer's input projection, [z | x B C | dt], go through the short
+ * causal convolution, the recurrence (step / verify / prefill above, or
+ * replayssm_prefill_packed) and the gated norm; replayssm_add_norm joins the
+ * block's output to the residual.  The conventions at the top of this file
+ * hold; a device range error goes to the sticky word of the state involved.
+ * ------------------------------------------------------------------------ */
+
+/* Convolution descriptor (host struct). */
+typedef struct rssm_conv_desc {
+    int32_t batch;        /* rows of a call: sequences with T tokens each, or packed sequences */
+    int32_t n_slots;      /* state slots S; 0 means S = batch */
+    int32_t n_heads;      /* H */
+    int32_t head_dim;     /* P (64) */
+    int32_t d_state;      /* N (128) */
+    int32_t n_groups;     /* G */
+    int32_t width;        /* W: taps, 2..4 */
+    int32_t max_draft;    /* Tmax: largest T of a speculative round, 1..8 */
+    int32_t in_dtype;     /* F32 | BF16: u, dt_raw, the outputs and the ring */
+    int32_t activation;   /* 0: none, 1: SiLU */
+    float dt_min, dt_max; /* clamp of dt after softplus (0 and infinity: none) */
+} rssm_conv_desc;
+
+/* Device buffers of one layer's convolution (host struct of device pointers).
+ * Channels Cc = H*P + 2*G*N, ordered x, B, C.  R = replayssm_conv_ring_rows. */
+typedef struct rssm_conv_state {
+    void *ring;           /* [S, R, Cc] in_dtype: recent raw inputs; zero it for an empty history */
+    int32_t *head;        /* [S] ring row of the slot's next token, 0..R-1; the W-1 rows before it
+                             (cyclically) are its history */
+    int32_t *work;        /* [S+1] library scratch: arrival counters + sticky error word; zero-initialise once */
+    const float *weight;  /* [W, Cc] taps; tap W-1 multiplies the current token */
+    const float *bias;    /* [Cc] or NULL */
+    const float *dt_bias; /* [H] or NULL */
+    const int32_t *slot_idx; /* [batch] slot of each row, -1 = padding row; NULL = row b uses slot b.
+                             Slots of one call must be distinct */
+} rssm_conv_state;
+
+/* Inputs and outputs of a convolution call.  u and dt_raw are views of the
+ * projection's rows: the tokens of a call follow each other (row-major over
+ * [batch, T]) at u_pitch / dt_pitch elements; outputs are dense in the layouts
+ * the recurrence reads. */
+typedef struct rssm_conv_io {
+    const void *u;        /* [tokens, Cc] raw x, B, C */
+    int64_t u_pitch;      /* >= Cc */
+    const void *dt_raw;   /* [tokens, H] */
+    int64_t dt_pitch;     /* >= H */
+    void *x, *B, *C, *dt; /* [tokens, H, P], [tokens, G, N], [tokens, G, N], [tokens, H] in_dtype */
+} rssm_conv_io;
+
+/*
+ * One decode token per row: with u_t the slot's t-th raw input,
+ *     c_t = bias + sum_{k<W} weight[k] u_{t-W+1+k},   out = silu(c_t) (or c_t)
+ *     dt  = min(max(softplus(dt_raw + dt_bias), dt_min), dt_max)
+ * in fp32, rounded once.  u_t goes into the ring at row head, and head
+ * advances by one.
+ */
+int replayssm_conv_step(const rssm_conv_desc *desc, const rssm_conv_state *st, const rssm_conv_io *io,
+                        hipStream_t stream);
+
+/* T draft positions per row, each seeing the drafts before it.  Their raw
+ * inputs go into ring rows head .. head+T-1; head stays.  1 <= T <= max_draft. */
+int replayssm_conv_verify(const rssm_conv_desc *desc, const rssm_conv_state *st, int32_t T,
+                          const rssm_conv_io *io, hipStream_t stream);
+
+/* Keep the first n_keep[b] verified positions: head += n_keep[b] (mod R).
+ * Values outside 0..T are clamped and flagged. */
+int replayssm_conv_accept(const rssm_conv_desc *desc, const rssm_conv_state *st, const int32_t *n_keep,
+                          int32_t T, hipStream_t stream);
+
+/*
+ * Packed prompts: row r holds tokens cu_seqlens[r] .. cu_seqlens[r+1]-1 of the
+ * `total` packed tokens (cu_seqlens [batch+1] int32 device, ascending within
+ * 0..total; offsets that do not are flagged, and what the call writes is then
+ * undefined).  A row starts from its slot's history, or from zeros where
+ * fresh[r] != 0 (fresh [batch] int32 device; NULL: from_zero for every row).
+ * The last W-1 inputs of history and prompt become the slot's history.  Rows
+ * without tokens leave their slot as it is; tokens of no row are skipped.
+ */
+int replayssm_conv_prefill(const rssm_conv_desc *desc, const rssm_conv_state *st, int64_t total,
+                           const int32_t *cu_seqlens, int32_t from_zero, const int32_t *fresh,
+                           const rssm_conv_io *io, hipStream_t stream);
+
+/* Ring rows R = max(W - 1 + Tmax, 2 (W - 1)) (0 for an invalid desc). */
+int32_t replayssm_conv_ring_rows(const rssm_conv_desc *desc);
+
+/* Validate a descriptor without launching anything. */
+int replayssm_conv_check_desc(const rssm_conv_desc *desc);
+
+/*
+ * Prefill of packed prompts of differing lengths: row r runs tokens
+ * cu_seqlens[r] .. cu_seqlens[r+1]-1 through the recurrence from its slot's
+ * checkpoint (the buffer must be empty, pos == 0, flagged otherwise) or from
+ * zero (fresh / from_zero as for replayssm_conv_prefill); the state after them
+ * becomes the checkpoint (pos = 0, intv + 1).  Rows without tokens leave their
+ * slot as it is.  Offsets outside 0 <= cu[r] <= cu[r+1] <= total are flagged
+ * and their row skipped.  Low-precision states as for replayssm_prefill.
+ * x [total,H,P], B, C [total,G,N], dt [total,H] (in_dtype); y [total,H,P] in
+ * y_dtype (F32, or BF16 rounded once) or NULL (then C may be NULL).
+ */
+int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_t total,
+                             const int32_t *cu_seqlens, int32_t from_zero, const int32_t *fresh,
+                             const void *x, const void *B, const void *C, const void *dt, void *y,
+                             int32_t y_dtype, hipStream_t stream);
+
+/*
+ * Gated norm behind the recurrence, over `groups` groups of dim / groups
+ * elements of each row:
+ *     v = y silu(z),  out = v rsqrt(mean(v^2) + eps) weight
+ * or, with norm_before_gate = 1, out = y rsqrt(mean(y^2) + eps) weight silu(z).
+ * y, out [rows, dim] dense; z [rows, dim] at z_pitch elements per row; weight
+ * [dim] fp32.  Each of y, z, out is F32 or BF16.  dim / groups <= 16384.
+ */
+int replayssm_gated_norm(int64_t rows, int32_t dim, int32_t groups, const void *y, int32_t y_dtype,
+                         const void *z, int32_t z_dtype, int64_t z_pitch, const float *weight, float eps,
+                         int32_t norm_before_gate, void *out, int32_t out_dtype, hipStream_t stream);
+
+/*
+ * Residual add and the norms after and before a block:
+ *     r = residual + scale f(x),  f(x) = x, or x rsqrt(mean(x^2) + eps) post_weight
+ *     residual_out = r,  out = r rsqrt(mean(r^2) + eps) weight
+ * The norm is taken of the fp32 r, before it is rounded to res_dtype.
+ * x, residual, residual_out (may be residual), out [rows, dim] dense; weight,
+ * post_weight [dim] fp32 (post_weight NULL: f(x) = x).  dim <= 16384.
+ */
+int replayssm_add_norm(int64_t rows, int32_t dim, const void *x, int32_t x_dtype, const void *residual,
+                       void *residual_out, int32_t res_dtype, const float *weight, const float *post_weight,
+                       float scale, float eps, void *out, int32_t out_dtype, hipStream_t stream);
+
 /* Buffer capacity Lcap = L + Tmax - 1 in entries (0 for an invalid desc). */
 size_t replayssm_buffer_capacity(const rssm_desc *desc);
 

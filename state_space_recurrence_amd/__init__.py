@@ -22,6 +22,7 @@ __all__ = [
     "F32", "BF16", "FP8_E4M3", "FP4_E2M1", "NONE", "ReplaySSMError", "lib", "LayerState",
     "step", "verify", "accept", "accept_deferred", "commit", "prefill", "load_checkpoint", "recurrent_step",
     "recurrent_verify", "recurrent_accept", "buffer_capacity", "check_device_errors",
+    "ConvState", "conv_step", "conv_verify", "conv_accept", "conv_prefill", "prefill_packed", "gated_norm", "add_norm",
 ]
 
 F32, BF16, FP8_E4M3, FP4_E2M1, NONE = 0, 1, 2, 3, 4
@@ -417,3 +418,7 @@ def recurrent_accept(pool_slots: int, sel, n_keep, T: int, *, heads: int = 1, gr
     desc = _make_desc(batch, heads, 64, 128, groups, 1, pool_slots - 1, torch.float32)
     _check(lib().replayssm_recurrent_accept(ctypes.byref(desc), _ptr(sel), _ptr(n_keep), T,
                                             _stream(stream)))
+
+
+from .mixer import (ConvState, add_norm, conv_accept, conv_prefill, conv_step, conv_verify,  # noqa: E402
+                    gated_norm, prefill_packed)

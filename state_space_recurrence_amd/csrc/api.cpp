@@ -7,12 +7,35 @@
 #include <cstdio>
 #include <cstring>
 
-#include "replayssm.h"
+#include "api_common.h"
 #include "kernels.h"
+#include "replayssm.h"
 
 namespace {
 
 thread_local char g_last_error[512] = "";
+
+constexpr int kMaxLcap = 64;       // step / accept / flush on F32 checkpoints
+constexpr int kMaxLcapVerify = 32; // verify, deferred commits and the low-precision formats
+constexpr int kMaxDraft = 8;
+
+int lcap_of(const rssm_desc *d) { return d->interval + d->max_draft - 1; }
+
+int heads_per_wg(const rssm_desc *d) {
+    const int hpg = d->n_heads / d->n_groups;
+    return hpg % 4 == 0 ? 4 : (hpg % 2 == 0 ? 2 : 1);
+}
+
+// Deferred accepts (declared by desc->deferred_commit) can leave up to Lcap
+// entries in a slot; a step on such a slot replays and commits one more.
+bool deferred_ok(const rssm_desc *d) { return d->deferred_commit == 1; }
+
+}  // namespace
+
+namespace rssm {
+namespace host {
+
+void clear_error() { g_last_error[0] = 0; }
 
 int fail(int status, const char *fmt, ...) {
     va_list ap;
@@ -27,19 +50,8 @@ int hip_status(hipError_t e, const char *what) {
     return fail(RSSM_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-constexpr int kMaxLcap = 64;       // step / accept / flush on F32 checkpoints
-constexpr int kMaxLcapVerify = 32; // verify, deferred commits and the low-precision formats
-constexpr int kMaxDraft = 8;
-
-int lcap_of(const rssm_desc *d) { return d->interval + d->max_draft - 1; }
-
 // State slots held by the buffers (rssm_desc.n_slots, 0 = batch).
 int nslots_of(const rssm_desc *d) { return d->n_slots > 0 ? d->n_slots : d->batch; }
-
-int heads_per_wg(const rssm_desc *d) {
-    const int hpg = d->n_heads / d->n_groups;
-    return hpg % 4 == 0 ? 4 : (hpg % 2 == 0 ? 2 : 1);
-}
 
 // Low-precision mode of a descriptor (rssm::SplitMode), or -1 for the fp32
 // checkpoint path.
@@ -49,10 +61,6 @@ int split_mode(const rssm_desc *d) {
     if (d->ckpt_dtype == RSSM_FP8_E4M3) return d->out_dtype == RSSM_FP4_E2M1 ? rssm::kSplitE4M3 : rssm::kLowE4M3;
     return -1;
 }
-
-// Deferred accepts (declared by desc->deferred_commit) can leave up to Lcap
-// entries in a slot; a step on such a slot replays and commits one more.
-bool deferred_ok(const rssm_desc *d) { return d->deferred_commit == 1; }
 
 int check_desc(const rssm_desc *d) {
     if (!d) return fail(RSSM_E_ARG, "desc is NULL");
@@ -155,11 +163,12 @@ rssm::ReplayParams replay_params(const rssm_desc *d, const rssm_state *s) {
     return p;
 }
 
-#define RSSM_TRY(expr)              \
-    do {                            \
-        int rc_ = (expr);           \
-        if (rc_ != RSSM_OK) return rc_; \
-    } while (0)
+}  // namespace host
+}  // namespace rssm
+
+using namespace rssm::host;
+
+namespace {
 
 // Low-precision step: outputs and appends, then the commit pass over the
 // slots whose interval that step closed.
@@ -173,7 +182,7 @@ int split_step(const rssm::ReplayParams &p, bool bf, int mode, hipStream_t strea
 extern "C" {
 
 int replayssm_check_desc(const rssm_desc *desc) {
-    g_last_error[0] = 0;
+    clear_error();
     return check_desc(desc);
 }
 
@@ -444,7 +453,8 @@ int replayssm_check_device_errors(const rssm_state *st, int32_t n_slots, hipStre
                         "check_device_errors clear"));
     return fail(RSSM_E_DEVICE,
                 "device range error flags 0x%x (1: position out of range, 2: n_keep out of range, "
-                "4: row mapped to a slot out of range, 8: two rows of one call on the same slot)",
+                "4: row mapped to a slot out of range, 8: two rows of one call on the same slot, "
+                "16: sequence offsets that do not ascend within the packed tokens)",
                 word);
 }
 

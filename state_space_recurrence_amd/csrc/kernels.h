@@ -30,6 +30,11 @@ struct ReplayParams {
     const int32_t *slot_idx;  // [batch] state slot of each call row, -1 = padding row; NULL = identity
     int nslots;             // state slots (ckpt / buffers / pos / intv / arrival counters)
     int from_zero;          // prefill: start from a zero state instead of the checkpoint
+    // packed prompts (row r holds tokens cu[r] .. cu[r+1]-1 of the packed inputs)
+    const int32_t *cu;      // [batch+1] sequence offsets
+    const int32_t *fresh;   // [batch] nonzero: the row starts from a zero state; NULL = from_zero for all
+    int64_t total;          // packed tokens
+    int y_bf16;             // packed outputs are bf16 (else fp32)
     int hpw;                // heads (waves) per workgroup
     int wg_per_slot;        // H / hpw
     // precision split (ignored by the fp32 kernels)
@@ -71,6 +76,9 @@ hipError_t launch_load_f32(const ReplayParams &p, hipStream_t s);   // ckpt[slot
 hipError_t launch_defer_accept(const ReplayParams &p, hipStream_t s);
 // p.T = prompt length; mode -1 = fp32 checkpoint, else the SplitMode of a low-precision state
 hipError_t launch_prefill(const ReplayParams &p, bool in_bf16, bool outputs, int mode, hipStream_t s);
+// Packed prompts on the vector units: any input type and state format, one
+// head's chunks in sequence.
+hipError_t launch_prefill_packed(const ReplayParams &p, bool in_bf16, bool outputs, int mode, hipStream_t s);
 hipError_t launch_split_step(const ReplayParams &p, bool in_bf16, int mode, hipStream_t s);
 hipError_t launch_split_verify(const ReplayParams &p, bool in_bf16, int mode, hipStream_t s);
 hipError_t launch_split_load(const ReplayParams &p, int mode, hipStream_t s);

@@ -84,13 +84,27 @@ __device__ __forceinline__ void quantize_chunk(const ReplayParams &a, const Slot
 }
 
 // MODE: -1 for the fp32 checkpoint, else the SplitMode of a low-precision state.
-template <typename TIn, bool OUT, int MODE>
+// PACKED: the rows' prompts differ in length and follow each other in the
+// inputs (offsets a.cu); outputs in fp32 or bf16.
+template <typename TIn, bool OUT, int MODE, bool PACKED>
 __global__ void __launch_bounds__(256) prefill_kernel(ReplayParams a) {
     __shared__ PrefillSmem sm;
 
     const Slot s = slot_of(a);
     if (s.b < 0) return;   // padding row
-    const int Tp = a.T;
+    int Tp = a.T;
+    size_t tok0 = (size_t)s.row * Tp;   // the row's first token in the inputs
+    if constexpr (PACKED) {
+        const int t_lo = a.cu[s.row], t_hi = a.cu[s.row + 1];
+        if (t_lo < 0 || t_hi < t_lo || t_hi > a.total) {
+            if (threadIdx.x == 0) atomicOr(a.err, kErrSeq);
+            return;
+        }
+        Tp = t_hi - t_lo;
+        tok0 = t_lo;
+        if (Tp == 0) return;   // no tokens: the slot is left as it is
+        if (a.fresh) a.from_zero = a.fresh[s.row] != 0;
+    }
     const HeadState sp = head_state(a.ckpt, s, a.H);
     const size_t hrow = ((size_t)s.b * a.H + s.h) * kP + s.hf;   // the lane's first row (low-precision state)
     float4 st[kChunks][kPerChunk];
@@ -114,11 +128,11 @@ __global__ void __launch_bounds__(256) prefill_kernel(ReplayParams a) {
         if (threadIdx.x == 0 && a.pos[s.b] != 0) atomicOr(a.err, kErrPos);   // buffer not empty
     }
     const size_t HP = (size_t)a.H * kP, GN = (size_t)a.G * kN;
-    const TIn *xin = reinterpret_cast<const TIn *>(a.x) + (size_t)s.row * Tp * HP + (size_t)s.h * kP;
-    const TIn *Bin = reinterpret_cast<const TIn *>(a.Bm) + (size_t)s.row * Tp * GN + (size_t)s.g * kN;
-    const TIn *Cin = reinterpret_cast<const TIn *>(a.Cm) + (size_t)s.row * Tp * GN + (size_t)s.g * kN;
-    const TIn *dtin = reinterpret_cast<const TIn *>(a.dt) + (size_t)s.row * Tp * a.H + s.h;
-    float *yout = a.y + (size_t)s.row * Tp * HP + (size_t)s.h * kP + s.prow;
+    const TIn *xin = reinterpret_cast<const TIn *>(a.x) + tok0 * HP + (size_t)s.h * kP;
+    const TIn *Bin = reinterpret_cast<const TIn *>(a.Bm) + tok0 * GN + (size_t)s.g * kN;
+    const TIn *Cin = reinterpret_cast<const TIn *>(a.Cm) + tok0 * GN + (size_t)s.g * kN;
+    const TIn *dtin = reinterpret_cast<const TIn *>(a.dt) + tok0 * a.H + s.h;
+    const size_t yo = tok0 * HP + (size_t)s.h * kP + s.prow;   // the lane's first output
     const float Ah = a.A[s.h], Dh = a.D[s.h];
     const int i_row = s.prow >> 1;   // the lane's row 2 i + hf in cs_index terms
 
@@ -206,7 +220,10 @@ __global__ void __launch_bounds__(256) prefill_kernel(ReplayParams a) {
                             const float term = sm.cy[s.wave][t][j] * sm.x[s.wave][j][s.prow];
                             yb += (j <= t) ? term : 0.f;
                         }
-                        yout[(size_t)(t0 + t) * HP] = sm.lam[s.wave][t] * y0 + yb;
+                        const size_t at = yo + (size_t)(t0 + t) * HP;
+                        const float yv = sm.lam[s.wave][t] * y0 + yb;
+                        if (PACKED && a.y_bf16) reinterpret_cast<__bf16 *>(a.y)[at] = (__bf16)yv;   // one rounding, RNE
+                        else a.y[at] = yv;
                     }
                 }
             }
@@ -231,31 +248,42 @@ __global__ void __launch_bounds__(256) prefill_kernel(ReplayParams a) {
 
 }  // namespace
 
-template <int MODE>
+template <int MODE, bool PACKED>
 static void launch_prefill_m(const ReplayParams &p, bool in_bf16, bool outputs, dim3 grid, dim3 block,
                              hipStream_t stream) {
     if (in_bf16) {
-        if (outputs) hipLaunchKernelGGL((prefill_kernel<uint16_t, true, MODE>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((prefill_kernel<uint16_t, false, MODE>), grid, block, 0, stream, p);
+        if (outputs) hipLaunchKernelGGL((prefill_kernel<uint16_t, true, MODE, PACKED>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((prefill_kernel<uint16_t, false, MODE, PACKED>), grid, block, 0, stream, p);
     } else {
-        if (outputs) hipLaunchKernelGGL((prefill_kernel<float, true, MODE>), grid, block, 0, stream, p);
-        else hipLaunchKernelGGL((prefill_kernel<float, false, MODE>), grid, block, 0, stream, p);
+        if (outputs) hipLaunchKernelGGL((prefill_kernel<float, true, MODE, PACKED>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((prefill_kernel<float, false, MODE, PACKED>), grid, block, 0, stream, p);
     }
+}
+
+template <bool PACKED>
+static hipError_t launch_prefill_any(const ReplayParams &p, bool in_bf16, bool outputs, int mode,
+                                     hipStream_t stream) {
+    dim3 grid(p.batch * p.wg_per_slot), block(64 * p.hpw);
+    switch (mode) {
+        case -1: launch_prefill_m<-1, PACKED>(p, in_bf16, outputs, grid, block, stream); break;
+        case kSplitBF16: launch_prefill_m<kSplitBF16, PACKED>(p, in_bf16, outputs, grid, block, stream); break;
+        case kSplitE4M3: launch_prefill_m<kSplitE4M3, PACKED>(p, in_bf16, outputs, grid, block, stream); break;
+        case kSharedFP4: launch_prefill_m<kSharedFP4, PACKED>(p, in_bf16, outputs, grid, block, stream); break;
+        case kLowBF16: launch_prefill_m<kLowBF16, PACKED>(p, in_bf16, outputs, grid, block, stream); break;
+        case kLowE4M3: launch_prefill_m<kLowE4M3, PACKED>(p, in_bf16, outputs, grid, block, stream); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
 }
 
 hipError_t launch_prefill(const ReplayParams &p, bool in_bf16, bool outputs, int mode, hipStream_t stream) {
     if (p.batch == 0 || p.T == 0) return hipSuccess;
-    dim3 grid(p.batch * p.wg_per_slot), block(64 * p.hpw);
-    switch (mode) {
-        case -1: launch_prefill_m<-1>(p, in_bf16, outputs, grid, block, stream); break;
-        case kSplitBF16: launch_prefill_m<kSplitBF16>(p, in_bf16, outputs, grid, block, stream); break;
-        case kSplitE4M3: launch_prefill_m<kSplitE4M3>(p, in_bf16, outputs, grid, block, stream); break;
-        case kSharedFP4: launch_prefill_m<kSharedFP4>(p, in_bf16, outputs, grid, block, stream); break;
-        case kLowBF16: launch_prefill_m<kLowBF16>(p, in_bf16, outputs, grid, block, stream); break;
-        case kLowE4M3: launch_prefill_m<kLowE4M3>(p, in_bf16, outputs, grid, block, stream); break;
-        default: return hipErrorInvalidValue;
-    }
-    return hipGetLastError();
+    return launch_prefill_any<false>(p, in_bf16, outputs, mode, stream);
+}
+
+hipError_t launch_prefill_packed(const ReplayParams &p, bool in_bf16, bool outputs, int mode, hipStream_t stream) {
+    if (p.batch == 0 || p.total == 0) return hipSuccess;
+    return launch_prefill_any<true>(p, in_bf16, outputs, mode, stream);
 }
 
 }  // namespace rssm

@@ -77,6 +77,8 @@ def scan(text: str, wait_states: int = WAIT_STATES):
         ws = 0
         for _, _, nxt in insts[i + 1:i + 1 + wait_states]:
             op = nxt.split()[0]
+            if op == "s_endpgm":   # nothing runs after it; what follows is another block
+                break
             parts = nxt.split(None, 1)
             if op.startswith("v_") and len(parts) > 1 and _vregs(parts[1].split(",")[0]) & dregs:
                 hits.append((fn, n, s, nxt))
