@@ -405,15 +405,23 @@ int replayssm_conv_check_desc(const rssm_conv_desc *desc);
  * checkpoint (the buffer must be empty, pos == 0, flagged otherwise) or from
  * zero (fresh / from_zero as for replayssm_conv_prefill); the state after them
  * becomes the checkpoint (pos = 0, intv + 1).  Rows without tokens leave their
- * slot as it is.  Offsets outside 0 <= cu[r] <= cu[r+1] <= total are flagged
- * and their row skipped.  Low-precision states as for replayssm_prefill.
+ * slot as it is.  Offsets that do not ascend within 0..total are flagged, and
+ * what the call writes is then undefined.  Low-precision states as for replayssm_prefill.
  * x [total,H,P], B, C [total,G,N], dt [total,H] (in_dtype); y [total,H,P] in
  * y_dtype (F32, or BF16 rounded once) or NULL (then C may be NULL).
+ * workspace: device scratch (16-byte aligned) of at least
+ * replayssm_prefill_packed_workspace bytes, which lets long sequences run in
+ * parallel pieces, or NULL: every sequence is then run from end to end.  Its
+ * contents are not kept between calls; calls that overlap need their own.
  */
 int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_t total,
                              const int32_t *cu_seqlens, int32_t from_zero, const int32_t *fresh,
                              const void *x, const void *B, const void *C, const void *dt, void *y,
-                             int32_t y_dtype, hipStream_t stream);
+                             int32_t y_dtype, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of device scratch for a replayssm_prefill_packed call of `total`
+ * tokens (0: none is used). */
+size_t replayssm_prefill_packed_workspace(const rssm_desc *desc, int64_t total);
 
 /*
  * Gated norm behind the recurrence, over `groups` groups of dim / groups

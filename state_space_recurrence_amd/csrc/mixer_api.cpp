@@ -10,6 +10,7 @@
 #include "kernels.h"
 #include "mixer.h"
 #include "replayssm.h"
+#include "scan.h"
 
 using namespace rssm::host;
 
@@ -134,6 +135,10 @@ int check_unit(const char *what, int64_t rows, int32_t dim, int32_t groups, floa
     return RSSM_OK;
 }
 
+// Packed prompts run on the matrix cores where their operands are exact: bf16
+// inputs, and a state that is fp32 on both sides of the call.
+bool on_matrix_cores(const rssm_desc *d) { return d->in_dtype == RSSM_BF16 && split_mode(d) < 0; }
+
 }  // namespace
 
 extern "C" {
@@ -191,10 +196,15 @@ int replayssm_conv_prefill(const rssm_conv_desc *desc, const rssm_conv_state *st
                       "conv prefill launch");
 }
 
+size_t replayssm_prefill_packed_workspace(const rssm_desc *desc, int64_t total) {
+    if (check_desc(desc) != RSSM_OK || total < 0 || total > (int64_t)1 << 30 || !on_matrix_cores(desc)) return 0;
+    return rssm::scan_workspace(total, desc->n_heads, desc->n_groups);
+}
+
 int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_t total,
                              const int32_t *cu_seqlens, int32_t from_zero, const int32_t *fresh,
                              const void *x, const void *B, const void *C, const void *dt, void *y,
-                             int32_t y_dtype, hipStream_t stream) {
+                             int32_t y_dtype, void *workspace, size_t workspace_bytes, hipStream_t stream) {
     RSSM_TRY(check_desc(desc));
     if (total < 0 || total > (int64_t)1 << 30 || total * desc->n_heads > (int64_t)1 << 31)
         return fail(RSSM_E_ARG, "prefill_packed: total outside 0..2^30, or total * n_heads over 2^31");
@@ -205,6 +215,9 @@ int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_
     if (!cu_seqlens) return fail(RSSM_E_ARG, "prefill_packed: cu_seqlens is NULL");
     if (!x || !B || !dt) return fail(RSSM_E_ARG, "prefill_packed: x / B / dt is NULL");
     if (y && !C) return fail(RSSM_E_ARG, "prefill_packed: outputs need C");
+    if (workspace && workspace_bytes < replayssm_prefill_packed_workspace(desc, total))
+        return fail(RSSM_E_ARG, "prefill_packed: a workspace of %zu bytes is smaller than "
+                    "replayssm_prefill_packed_workspace", workspace_bytes);
     rssm::ReplayParams p = replay_params(desc, st);
     p.x = x;
     p.Bm = B;
@@ -216,6 +229,8 @@ int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_
     p.cu = cu_seqlens;
     p.fresh = fresh;
     p.total = total;
+    if (on_matrix_cores(desc))
+        return hip_status(rssm::launch_scan(p, y != nullptr, workspace, stream), "packed prefill launch");
     return hip_status(rssm::launch_prefill_packed(p, desc->in_dtype == RSSM_BF16, y != nullptr, split_mode(desc),
                                                   stream),
                       "packed prefill launch");

@@ -1,0 +1,45 @@
+// scan.h -- host interface of the matrix-core scan of packed prompts.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kernels.h"
+
+namespace rssm {
+
+constexpr int kScanChunk = 64;       // tokens per chunk
+constexpr int kScanHeads = 2;        // heads per workgroup (of one B/C group)
+
+struct ScanParams {
+    ReplayParams r;
+    float *loc;        // [nfull, H, P, N] end state of each full segment that has a successor
+    float *s0;         // [nfull, H, P, N] copy of the start state of a split sequence (at its first segment's entry)
+    float *lam;        // [nfull, H] decay over the segment
+    int lseg;          // tokens per segment (a multiple of kScanChunk)
+    int nseg;          // segment entries in the grid: total / lseg + batch
+    int nfull;         // full segments that fit: total / lseg
+    int hb;            // workgroups per (segment, group)
+};
+
+// Tokens per segment for a call: long sequences are cut so that the card's
+// compute units all have work.
+inline int scan_segment(int64_t total, int H, int G) {
+    const int64_t hb = (int64_t)G * ((H / G + kScanHeads - 1) / kScanHeads);
+    const int64_t chunks = (total + kScanChunk - 1) / kScanChunk;
+    int64_t per = (chunks * hb + 511) / 512;   // chunks per workgroup with two workgroups on every CU
+    if (per < 4) per = 4;
+    return (int)(per * kScanChunk);
+}
+
+inline size_t scan_workspace(int64_t total, int H, int G) {
+    const int64_t nfull = total / scan_segment(total, H, G);
+    // a single segment never has a successor
+    return nfull == 0 ? 0 : (size_t)nfull * H * (2 * 64 * 128 + 1) * sizeof(float);
+}
+
+// bf16 inputs, fp32 checkpoints.  p.loc etc. may be NULL when workspace is
+// absent: every sequence is then one segment.
+hipError_t launch_scan(const ReplayParams &p, bool outputs, void *workspace, hipStream_t s);
+
+}  // namespace rssm

@@ -1,0 +1,513 @@
+// scan_kernels.hip -- packed prompts through the recurrence on the matrix
+// cores (bf16 inputs, fp32 checkpoints).
+//
+// A sequence is taken in chunks of 64 tokens.  With l_i = A dt_i, c_t the sum
+// of l over the chunk up to t, and S the state before the chunk:
+//     M_tj = (C_t . B_j) dt_j exp(c_t - c_j)  for j <= t, plus D at j = t
+//     y_t  = sum_j M_tj x_j + exp(c_t) S C_t
+//     S'   = exp(c_63) S + sum_j dt_j exp(c_63 - c_j) x_j (outer) B_j
+// One wave owns 32 of the 64 state rows p of a head and keeps its half of the
+// state, transposed [n][p], in the accumulators of v_mfma_f32_32x32x16_bf16
+// for the whole segment.  An accumulator holds 4 consecutive rows per lane
+// half, a matrix operand 8; the products' inner index may run in any order, so
+// every operand in LDS is stored with quads 1 and 2 of each 16 exchanged and
+// accumulators (the state for S C, the decayed Gram tile for M x) feed the
+// next product straight from registers.
+//
+// Precision.  x, B, C are bf16 and exact operands.  Values formed in fp32
+// (state, M, weighted x) are split into bf16 parts, v = hi + mid + lo, and
+// multiplied part by part into the same fp32 accumulator: three parts carry
+// all 24 bits, two carry 16.  The state always uses three, so it is as exact
+// as an fp32 update; y uses three for fp32 outputs and two for bf16 ones,
+// whose own rounding is 2^-8.  Decay sums run in fp64 and are kept as two
+// floats: a difference of two long sums would otherwise lose the bits of a
+// short one.
+//
+// Long sequences.  When sequences x heads do not fill the card, a sequence is
+// cut into segments: a first launch leaves each segment's end state (the first
+// from the slot's state, the others from zero), and in the second every
+// segment joins the states before it, S = loc_{k-1} + lam_{k-1} (loc_{k-2} +
+// ...), before it runs its tokens.
+#include "device_common.h"
+#include "mixer_device.h"
+#include "replay_common.h"
+#include "scan.h"
+
+namespace rssm {
+namespace {
+
+constexpr int kQ = kScanChunk;
+constexpr int kRowN = 136;   // elements of an LDS row of 128: 16 bytes more, so that 16 rows start in different banks
+constexpr int kRowQ = 72;    // elements of an LDS row of 64
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef unsigned int u2v __attribute__((ext_vector_type(2)));
+
+struct ScanSmem {
+    uint16_t B[kQ][kRowN];            // B_j[n], n exchanged
+    uint16_t C[kQ][kRowN];            // C_t[n], n exchanged
+    uint16_t BT[kN][kRowQ];           // B_j[n] as [n][j], j exchanged
+    uint16_t XT[kScanHeads][kP][kRowQ];   // x_j[p] as [p][j], j exchanged
+    float chi[4][kQ], clo[4][kQ];     // per wave: c_t / ln 2 as two floats
+    float dt[4][kQ];                  // dt_j
+    float cf[4][kQ];                  // dt_j exp(c_31 - c_j), j < 32
+    float w[4][kQ];                   // dt_j exp(c_63 - c_j)
+    int bad;                          // first token of the chunk with a non-finite x
+};
+
+// Position of quad q (4 elements) among the quads of a row: 1 and 2 of each four exchanged.
+__device__ __forceinline__ int quad_at(int q) { return (q & ~3) | ((q & 1) << 1) | ((q >> 1) & 1); }
+
+__device__ __forceinline__ b8v operand(const uint16_t *p) {
+    return __builtin_bit_cast(b8v, *reinterpret_cast<const u4v *>(p));
+}
+
+typedef float f2v __attribute__((ext_vector_type(2)));
+typedef __bf16 b2v __attribute__((ext_vector_type(2)));
+
+// v = part[0] + part[1] + ... to 8 NP bits (each part one rounding, two values an instruction)
+template <int NP>
+__device__ __forceinline__ void split(f8v v, b8v (&part)[NP]) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        u4v u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            u[i] = __builtin_bit_cast(unsigned, __builtin_convertvector(f2v{v[2 * i], v[2 * i + 1]}, b2v));
+            if (k + 1 < NP) {
+                v[2 * i] -= __uint_as_float(u[i] << 16);
+                v[2 * i + 1] -= __uint_as_float(u[i] & 0xFFFF0000u);
+            }
+        }
+        part[k] = __builtin_bit_cast(b8v, u);
+    }
+}
+
+__device__ __forceinline__ f16v mfma(b8v a, b8v b, f16v c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f8v half_of(const f16v &v, int s) {
+    f8v r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = v[8 * s + i];
+    return r;
+}
+
+__device__ __forceinline__ f8v read8(const float *p) {   // p[0..3], p[8..11]
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 8);
+    return f8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
+// Column i of four rows of eight 16-bit values.
+template <int I>
+__device__ __forceinline__ u2v column(u4v a, u4v b, u4v c, u4v d) {
+    constexpr unsigned sel = I & 1 ? 0x07060302 : 0x05040100;
+    return u2v{__builtin_amdgcn_perm(b[I / 2], a[I / 2], sel), __builtin_amdgcn_perm(d[I / 2], c[I / 2], sel)};
+}
+
+// The four rows' columns 0..7 to LDS rows p, p + kRowQ, ...
+template <int I = 0>
+__device__ __forceinline__ void store_columns(uint16_t *p, u4v a, u4v b, u4v c, u4v d) {
+    *reinterpret_cast<u2v *>(p + I * kRowQ) = column<I>(a, b, c, d);
+    if constexpr (I < 7) store_columns<I + 1>(p, a, b, c, d);
+}
+
+// A state tile from and to memory: values 4 i .. 4 i + 3 at s + 8 i.
+__device__ __forceinline__ void add_tile(f16v &v, const float *s, float f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 u = *reinterpret_cast<const float4 *>(s + 8 * i);
+        v[4 * i] += f * u.x;
+        v[4 * i + 1] += f * u.y;
+        v[4 * i + 2] += f * u.z;
+        v[4 * i + 3] += f * u.w;
+    }
+}
+
+__device__ __forceinline__ void put_tile(const f16v &v, float *s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4 *>(s + 8 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// Inclusive sum over lanes 0..l.
+__device__ __forceinline__ double prefix(double v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const double o = __shfl_up(v, d);
+        if (lane >= d) v += o;
+    }
+    return v;
+}
+
+// Last sequence s whose first segment entry, cu[s] / lseg + s, is <= j (the
+// entries of a sequence follow it; consecutive sequences never overlap).
+__device__ __forceinline__ int segment_owner(const ScanParams &a, int j, int lane) {
+    int lo = 0, n = a.r.batch;   // the answer is in lo .. lo + n - 1
+    while (n > 1) {
+        const int step = (n + 63) / 64;
+        const int s = lo + lane * step;
+        const bool le = lane * step < n && a.r.cu[s] / a.lseg + s <= j;
+        const uint64_t m = __ballot(le);
+        const int k = m ? 63 - __builtin_clzll(m) : 0;
+        n = n - k * step < step ? n - k * step : step;
+        lo += k * step;
+    }
+    return lo;
+}
+
+// YP: bf16 parts of M and the state in y; OUT: outputs wanted; LOCAL: the
+// first launch, which leaves the end states of segments with a successor.
+template <typename TY, int YP, bool OUT, bool LOCAL>
+__global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
+    __shared__ __attribute__((aligned(16))) ScanSmem sm;
+    const ReplayParams &r = a.r;
+    const int lane = threadIdx.x & 63, c = lane & 31, hf = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hpg = r.H / r.G;
+
+    if (!LOCAL && blockIdx.x == 0)   // offsets that do not ascend (the mapping below stays within the tensors)
+        for (int i = threadIdx.x; i <= r.batch; i += 256)
+            if (r.cu[i] < 0 || r.cu[i] > r.total || (i && r.cu[i] < r.cu[i - 1])) atomicOr(r.err, kErrSeq);
+
+    // Workgroups of one (segment, group) read the same B and C: they follow
+    // each other on one XCD, and the pairs are dealt to the XCDs in turn.
+    const int npair = a.nseg * r.G;
+    const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
+    const int pair = (at / a.hb) * 8 + xcd, hblk = at % a.hb;
+    if (pair >= npair) return;
+    const int entry = pair / r.G, g = pair - entry * r.G;
+
+    const int seq = __builtin_amdgcn_readfirstlane(segment_owner(a, entry, lane));
+    const int start = r.cu[seq], end = r.cu[seq + 1];
+    if (start < 0 || end > r.total || end <= start) return;
+    const int k = entry - (start / a.lseg + seq);
+    if (k < 0 || (int64_t)k * a.lseg >= end - start) return;
+    const int tok0 = start + k * a.lseg;
+    const int len = end - tok0 < a.lseg ? end - tok0 : a.lseg;
+    const bool last = tok0 + len == end;
+    if (LOCAL && last) return;
+    const int b = slot_of_row(r, seq);
+    if (b < 0) return;   // padding row
+
+    const int hh = wave >> 1;                  // the wave's head among the workgroup's
+    const int hl = hblk * kScanHeads + hh;     // ... within the group
+    const bool live = hl < hpg;                // an odd head count leaves half a workgroup idle
+    const int h = g * hpg + (live ? hl : hpg - 1);
+    const int p0 = (wave & 1) * 32;            // the wave's state rows
+    const size_t HP = (size_t)r.H * kP, GN = (size_t)r.G * kN;
+
+    // ---- state before the segment: st[nt][i] = S[p0 + c][32 nt + 8 (i / 4) + 4 hf + i % 4]
+    f16v st0 = (f16v)0.f, st1 = (f16v)0.f, st2 = (f16v)0.f, st3 = (f16v)0.f;
+    const size_t cell = (size_t)(p0 + c) * kN + 4 * hf;
+    auto add_state = [&](const float *s, float f) {
+        add_tile(st0, s + cell, f);
+        add_tile(st1, s + cell + 32, f);
+        add_tile(st2, s + cell + 64, f);
+        add_tile(st3, s + cell + 96, f);
+    };
+    auto put_state = [&](float *s) {
+        put_tile(st0, s + cell);
+        put_tile(st1, s + cell + 32);
+        put_tile(st2, s + cell + 64);
+        put_tile(st3, s + cell + 96);
+    };
+    const size_t headN = (size_t)kP * kN;
+    float *ckpt = r.ckpt + ((size_t)b * r.H + h) * headN;
+    const size_t ent0 = (size_t)(start / a.lseg);   // the sequence's first full segment in the workspace
+    if (k == 0) {
+        const bool fresh = r.fresh ? r.fresh[seq] != 0 : r.from_zero != 0;
+        if (!fresh) {
+            add_state(LOCAL || last ? ckpt : a.s0 + (ent0 * r.H + h) * headN, 1.f);
+            if ((LOCAL || last) && threadIdx.x == 0 && r.pos[b] != 0) atomicOr(r.err, kErrPos);   // buffer not empty
+            // the second launch rewrites the checkpoint, so its first segment reads a copy
+            if (LOCAL && live) put_state(a.s0 + (ent0 * r.H + h) * headN);
+        }
+    } else if (!LOCAL) {
+        // a factor of exactly zero ends the sum: nothing before it counts
+        float f = 1.f;
+        for (int i = k - 1; i >= 0 && f != 0.f; --i) {
+            const size_t e = (ent0 + i) * r.H + h;
+            add_state(a.loc + e * headN, f);
+            f *= a.lam[e];
+        }
+    }
+
+    const uint16_t *xin = reinterpret_cast<const uint16_t *>(r.x) + (size_t)tok0 * HP;
+    const uint16_t *Bin = reinterpret_cast<const uint16_t *>(r.Bm) + (size_t)tok0 * GN + (size_t)g * kN;
+    const uint16_t *Cin = reinterpret_cast<const uint16_t *>(r.Cm) + (size_t)tok0 * GN + (size_t)g * kN;
+    const uint16_t *dtin = reinterpret_cast<const uint16_t *>(r.dt) + (size_t)tok0 * r.H + h;
+    TY *yout = reinterpret_cast<TY *>(r.y) + (size_t)tok0 * HP + (size_t)h * kP + p0 + 4 * hf;
+    const double A2 = (double)r.A[h] * 1.4426950408889634;
+    const float Dh = r.D[h];
+
+    // ---- staging roles: 16 quads of tokens x 16 octets of n (B, C); 2 heads x 16 quads x 8 octets of p (x)
+    const int bo = threadIdx.x & 15, bq = threadIdx.x >> 4;
+    const int xo = threadIdx.x & 7, xq = (threadIdx.x >> 3) & 15, xh = threadIdx.x >> 7;
+    const int xhl = hblk * kScanHeads + xh;
+    const size_t xcol = (size_t)(g * hpg + (xhl < hpg ? xhl : hpg - 1)) * kP + 8 * xo;
+    u4v rB[4], rC[4], rX[4];
+    float rdt;
+    // Lane offsets (bytes) from the chunk's first row, which is uniform: a
+    // chunk spans less than 4 GiB, so 32 bits do.
+    const unsigned bpitch = (unsigned)GN * 2, xpitch = (unsigned)HP * 2;
+    const unsigned boff = 16 * bo, xoff = (unsigned)xcol * 2;
+    auto fetch = [&](int t0) {   // chunk at t0; tokens past the segment are zeros
+        const int rem = len - t0;
+        const char *bp = reinterpret_cast<const char *>(Bin + (size_t)t0 * GN);
+        const char *cp = reinterpret_cast<const char *>(Cin + (size_t)t0 * GN);
+        const char *xp = reinterpret_cast<const char *>(xin + (size_t)t0 * HP);
+        if (rem >= kQ) {
+            const unsigned bv = boff + 4 * bq * bpitch, xv = xoff + 4 * xq * xpitch;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                rB[i] = *reinterpret_cast<const u4v *>(bp + i * bpitch + bv);
+                if (OUT) rC[i] = *reinterpret_cast<const u4v *>(cp + i * bpitch + bv);
+                rX[i] = *reinterpret_cast<const u4v *>(xp + i * xpitch + xv);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int tb = 4 * bq + i, tx = 4 * xq + i;
+                rB[i] = rX[i] = (u4v)0u;
+                if (OUT) rC[i] = (u4v)0u;
+                if (tb < rem) {
+                    rB[i] = *reinterpret_cast<const u4v *>(bp + (boff + tb * bpitch));
+                    if (OUT) rC[i] = *reinterpret_cast<const u4v *>(cp + (boff + tb * bpitch));
+                }
+                if (tx < rem) rX[i] = *reinterpret_cast<const u4v *>(xp + (xoff + tx * xpitch));
+            }
+        }
+        rdt = lane < rem ? vec8<uint16_t>::get(dtin + (size_t)t0 * r.H + (unsigned)(lane * r.H)) : 0.f;
+    };
+
+    double total = 0.0;   // decay of the segment (LOCAL)
+    fetch(0);
+    for (int t0 = 0; t0 < len;) {
+        __syncthreads();   // the previous chunk's LDS reads are done
+        if (threadIdx.x == 0) sm.bad = kQ;
+        {
+            store_columns(&sm.BT[8 * bo][4 * quad_at(bq)], rB[0], rB[1], rB[2], rB[3]);
+            if (OUT) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n0 = 4 * quad_at(2 * bo), n1 = 4 * quad_at(2 * bo + 1);
+                    *reinterpret_cast<u2v *>(&sm.B[4 * bq + i][n0]) = u2v{rB[i].x, rB[i].y};
+                    *reinterpret_cast<u2v *>(&sm.B[4 * bq + i][n1]) = u2v{rB[i].z, rB[i].w};
+                    *reinterpret_cast<u2v *>(&sm.C[4 * bq + i][n0]) = u2v{rC[i].x, rC[i].y};
+                    *reinterpret_cast<u2v *>(&sm.C[4 * bq + i][n1]) = u2v{rC[i].z, rC[i].w};
+                }
+            }
+            store_columns(&sm.XT[xh][8 * xo][4 * quad_at(xq)], rX[0], rX[1], rX[2], rX[3]);
+        }
+        int q = len - t0 < kQ ? len - t0 : kQ;   // tokens of this chunk
+        if (OUT) {
+            // M_tj = 0 for j > t does not keep a non-finite x_j out of y_t: a
+            // chunk ends before a token that holds one, which is then taken alone.
+            __syncthreads();
+            unsigned seen = 0;
+            int first = kQ;
+#pragma unroll
+            for (int i = 3; i >= 0; --i) {
+                unsigned bits = 0;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) bits |= (rX[i][d] & 0x7F807F80u) + 0x00800080u;
+                if (bits & 0x80008000u) first = 4 * xq + i;
+                seen |= bits;
+            }
+            if (seen & 0x80008000u) atomicMin(&sm.bad, first);
+        }
+        __syncthreads();
+        if (OUT) {
+            const int stop = sm.bad > 0 ? sm.bad : 1;
+            if (stop < q) {
+                q = stop;
+                for (int i = threadIdx.x; i < kScanHeads * kP * kQ; i += 256) {
+                    const int j = i & (kQ - 1), p = (i >> 6) & (kP - 1);
+                    if (j >= q) sm.XT[i >> 12][p][4 * quad_at(j >> 2) + (j & 3)] = 0;
+                }
+                if (lane >= q) rdt = 0.f;
+                __syncthreads();
+            }
+        }
+
+        // ---- decays of the wave's head (both waves of a head compute them)
+        const double cum = prefix(A2 * (double)rdt, lane);
+        const double c31 = __shfl(cum, 31), c63 = __shfl(cum, 63);
+        {
+            const float hi = (float)cum;
+            sm.chi[wave][lane] = hi;
+            sm.clo[wave][lane] = (float)(cum - (double)hi);
+            sm.dt[wave][lane] = rdt;
+            sm.cf[wave][lane] = lane < 32 ? rdt * __builtin_amdgcn_exp2f((float)(c31 - cum)) : 0.f;
+            sm.w[wave][lane] = rdt * __builtin_amdgcn_exp2f((float)(c63 - cum));
+        }
+        const float lam = __builtin_amdgcn_exp2f((float)c63);
+        total += c63;
+        const int t1 = t0 + q;
+        __builtin_amdgcn_wave_barrier();
+        if (!OUT && t1 < len) fetch(t1);
+
+        if (OUT && live) {
+            // ---- y^T[p][t] = sum_n S[p][n] C_t[n] and the Gram tiles G^T[j][t] = B_j . C_t
+            f16v y0 = (f16v)0.f, y1 = (f16v)0.f, g00 = (f16v)0.f, g01 = (f16v)0.f, g11 = (f16v)0.f;
+            auto step = [&](const f16v &tile, int ks) {
+                b8v s[YP];
+                split<YP>(half_of(tile, ks & 1), s);
+                const b8v b0 = operand(&sm.B[c][16 * ks + 8 * hf]), b1 = operand(&sm.B[32 + c][16 * ks + 8 * hf]);
+                const b8v c0 = operand(&sm.C[c][16 * ks + 8 * hf]), c1 = operand(&sm.C[32 + c][16 * ks + 8 * hf]);
+                g00 = mfma(b0, c0, g00);
+                g01 = mfma(b0, c1, g01);
+                g11 = mfma(b1, c1, g11);
+#pragma unroll
+                for (int i = YP - 1; i >= 0; --i) {
+                    y0 = mfma(s[i], c0, y0);
+                    y1 = mfma(s[i], c1, y1);
+                }
+            };
+            step(st0, 0);
+            step(st0, 1);
+            step(st1, 2);
+            step(st1, 3);
+            step(st2, 4);
+            step(st2, 5);
+            step(st3, 6);
+            step(st3, 7);
+            // the next chunk is requested here, when the state's parts are done with
+            if (t1 < len) fetch(t1);
+            const float h0 = sm.chi[wave][c], l0 = sm.clo[wave][c];
+            const float h1 = sm.chi[wave][32 + c], l1 = sm.clo[wave][32 + c];
+            const float hm = sm.chi[wave][31], lm = sm.clo[wave][31];
+            const float e0 = __builtin_amdgcn_exp2f(h0 + l0), e1 = __builtin_amdgcn_exp2f(h1 + l1);
+            const float rf = __builtin_amdgcn_exp2f((h1 - hm) + (l1 - lm));   // exp(c_t - c_31)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                y0[i] *= e0;
+                y1[i] *= e1;
+            }
+            // ---- y^T += x^T M^T, M^T as the operand straight from the Gram accumulators
+            auto apply = [&](const f16v &gram, int jt, float ht, float lt, bool diag, f16v &y) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const int j0 = 32 * jt + 16 * s + 4 * hf;
+                    f8v m = half_of(gram, s);
+                    if (diag) {
+                        const f8v ch = read8(&sm.chi[wave][j0]), cl = read8(&sm.clo[wave][j0]);
+                        const f8v d = read8(&sm.dt[wave][j0]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int j = 16 * s + 4 * hf + 8 * (i >> 2) + (i & 3);
+                            const float e = __builtin_amdgcn_exp2f((ht - ch[i]) + (lt - cl[i]));
+                            m[i] = j <= c ? m[i] * (d[i] * e) : 0.f;
+                            m[i] += j == c ? Dh : 0.f;
+                        }
+                    } else {
+                        const f8v f = read8(&sm.cf[wave][j0]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) m[i] *= f[i] * rf;
+                    }
+                    b8v part[YP];
+                    split<YP>(m, part);
+                    const b8v x = operand(&sm.XT[hh][p0 + c][32 * jt + 16 * s + 8 * hf]);
+#pragma unroll
+                    for (int i = YP - 1; i >= 0; --i) y = mfma(x, part[i], y);
+                }
+            };
+            apply(g00, 0, h0, l0, true, y0);
+            apply(g01, 0, h1, l1, false, y1);
+            apply(g11, 1, h1, l1, true, y1);
+            auto store = [&](const f16v &y, int t) {
+                if (t >= q) return;
+                TY *o = yout + (size_t)(t0 + t) * HP;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (sizeof(TY) == 4) {
+                        *reinterpret_cast<float4 *>(o + 8 * i) =
+                            make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    } else {
+                        typedef float f4x __attribute__((ext_vector_type(4)));
+                        typedef __bf16 b4x __attribute__((ext_vector_type(4)));
+                        *reinterpret_cast<u2v *>(o + 8 * i) = __builtin_bit_cast(
+                            u2v, __builtin_convertvector(f4x{y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]}, b4x));
+                    }
+                }
+            };
+            store(y0, c);
+            store(y1, 32 + c);
+        } else if (OUT && t1 < len) {
+            fetch(t1);
+        }
+
+        // ---- S^T[n][p] = exp(c_63) S^T + sum_j B_j[n] (w_j x_j[p])
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            st0[i] *= lam;
+            st1[i] *= lam;
+            st2[i] *= lam;
+            st3[i] *= lam;
+        }
+#pragma unroll
+        for (int js = 0; js < 4; ++js) {
+            f8v v = vec8<uint16_t>::widen(*reinterpret_cast<const u4v *>(&sm.XT[hh][p0 + c][16 * js + 8 * hf]));
+            const f8v w = read8(&sm.w[wave][16 * js + 4 * hf]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= w[i];
+            b8v part[3];
+            split<3>(v, part);
+            const uint16_t *bt = &sm.BT[c][16 * js + 8 * hf];
+            const b8v b0 = operand(bt), b1 = operand(bt + 32 * kRowQ), b2 = operand(bt + 64 * kRowQ),
+                      b3 = operand(bt + 96 * kRowQ);
+#pragma unroll
+            for (int i = 2; i >= 0; --i) {
+                st0 = mfma(b0, part[i], st0);
+                st1 = mfma(b1, part[i], st1);
+                st2 = mfma(b2, part[i], st2);
+                st3 = mfma(b3, part[i], st3);
+            }
+        }
+        t0 = t1;
+    }
+
+    if (LOCAL) {
+        const size_t e = (ent0 + k) * r.H + h;
+        if (live) {
+            put_state(a.loc + e * headN);
+            if ((wave & 1) == 0 && lane == 0) a.lam[e] = exp2f((float)total);
+        }
+    } else if (last) {
+        if (live) put_state(ckpt);
+        publish_position(r, b, 0, true, -1);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_scan(const ReplayParams &p, bool outputs, void *workspace, hipStream_t s) {
+    if (p.batch == 0 || p.total == 0) return hipSuccess;
+    ScanParams a{};
+    a.r = p;
+    a.lseg = scan_segment(p.total, p.H, p.G);
+    a.nfull = (int)(p.total / a.lseg);
+    if (!workspace || a.nfull == 0) {   // one segment per sequence
+        a.lseg = (int)((p.total + kScanChunk) / kScanChunk * kScanChunk);
+        a.nfull = 0;
+    } else {
+        a.loc = static_cast<float *>(workspace);
+        a.s0 = a.loc + (size_t)a.nfull * p.H * kP * kN;
+        a.lam = a.s0 + (size_t)a.nfull * p.H * kP * kN;
+    }
+    a.nseg = (int)(p.total / a.lseg) + p.batch;
+    a.hb = (p.H / p.G + kScanHeads - 1) / kScanHeads;
+    a.r.wg_per_slot = p.G * a.hb;
+    const int64_t blocks = ((int64_t)a.nseg * p.G + 7) / 8 * 8 * a.hb;
+    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks), block(256);
+    if (a.nfull) hipLaunchKernelGGL((scan_kernel<float, 3, false, true>), grid, block, 0, s, a);
+    if (!outputs) hipLaunchKernelGGL((scan_kernel<float, 3, false, false>), grid, block, 0, s, a);
+    else if (p.y_bf16) hipLaunchKernelGGL((scan_kernel<uint16_t, 2, true, false>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((scan_kernel<float, 3, true, false>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace rssm

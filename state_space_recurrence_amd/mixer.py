@@ -53,7 +53,10 @@ def _lib():
         L.replayssm_conv_prefill.argtypes = [_CD, _CS, _i64, _vp, _i32, _vp, _CI, _vp]
         L.replayssm_conv_ring_rows.argtypes = [_CD]
         L.replayssm_conv_check_desc.argtypes = [_CD]
-        L.replayssm_prefill_packed.argtypes = [_vp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp]
+        L.replayssm_prefill_packed.argtypes = [_vp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
+                                               ctypes.c_size_t, _vp]
+        L.replayssm_prefill_packed_workspace.argtypes = [_vp, _i64]
+        L.replayssm_prefill_packed_workspace.restype = ctypes.c_size_t
         L.replayssm_gated_norm.argtypes = [_i64, _i32, _i32, _vp, _i32, _vp, _i32, _i64, _vp, _f32, _i32, _vp, _i32,
                                            _vp]
         L.replayssm_add_norm.argtypes = [_i64, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _f32, _f32, _vp, _i32, _vp]
@@ -234,6 +237,20 @@ def conv_prefill(cs: ConvState, u, dt, cu_seqlens, *, from_zero: bool = False, f
     return out
 
 
+def _workspace(ls: LayerState, need: int, device, stream):
+    """The layer's scratch, kept between calls and grown when a call needs more.
+    Calls on one layer are ordered, so they can share it; a stream other than
+    the one it was allocated on is noted with the allocator."""
+    at = torch.cuda.current_stream() if stream is None else stream
+    ws, home = getattr(ls, "_packed_ws", (None, None))
+    if ws is None or ws.numel() < need:
+        ws, home = _empty((need,), torch.uint8, device, at), at.cuda_stream
+        ls._packed_ws = (ws, home)
+    elif home != at.cuda_stream:
+        ws.record_stream(at)
+    return ws
+
+
 def prefill_packed(ls: LayerState, x, B, C, dt, cu_seqlens, *, from_zero: bool = False, fresh=None,
                    outputs: bool = True, y=None, y_dtype: torch.dtype = torch.float32, stream=None, slots=None):
     """Packed prompts into the checkpoints (replayssm_prefill_packed): x
@@ -260,10 +277,13 @@ def prefill_packed(ls: LayerState, x, B, C, dt, cu_seqlens, *, from_zero: bool =
         _need(y, (total, ls.heads, ls.head_dim), y.dtype, "y")
     else:
         y = None
-    _check(_lib().replayssm_prefill_packed(ctypes.addressof(d), ctypes.addressof(st), total, cu_seqlens.data_ptr(),
-                                           int(from_zero), _ptr(fresh), x.data_ptr(), B.data_ptr(), _ptr(C),
-                                           dt.data_ptr(), _ptr(y), F32 if y is None else _TYPES[y.dtype],
-                                           _raw_stream(stream)))
+    L = _lib()
+    need = L.replayssm_prefill_packed_workspace(ctypes.addressof(d), total)
+    ws = _workspace(ls, need, x.device, stream) if need else None
+    _check(L.replayssm_prefill_packed(ctypes.addressof(d), ctypes.addressof(st), total, cu_seqlens.data_ptr(),
+                                      int(from_zero), _ptr(fresh), x.data_ptr(), B.data_ptr(), _ptr(C),
+                                      dt.data_ptr(), _ptr(y), F32 if y is None else _TYPES[y.dtype],
+                                      _ptr(ws), need, _raw_stream(stream)))
     return y
 
 

@@ -12,6 +12,7 @@
 #include "api_common.h"
 #include "mixer.h"
 #include "replayssm.h"
+#include "scan.h"
 
 static char g_error[512];
 
@@ -43,6 +44,7 @@ RSSM_STUB(hipError_t launch_conv_packed(const ConvParams &, bool, int, hipStream
 RSSM_STUB(hipError_t launch_conv_accept(const ConvParams &, hipStream_t))
 RSSM_STUB(hipError_t launch_gated_norm(const GatedNormParams &, bool, bool, bool, hipStream_t))
 RSSM_STUB(hipError_t launch_add_norm(const AddNormParams &, bool, bool, bool, hipStream_t))
+RSSM_STUB(hipError_t launch_scan(const ReplayParams &, bool, void *, hipStream_t))
 RSSM_STUB(hipError_t launch_prefill_packed(const ReplayParams &, bool, bool, int, hipStream_t))
 }  // namespace rssm
 
@@ -87,14 +89,14 @@ int main() {
     rssm_state ls{};
     l.batch = 1;
     l.n_heads = 0x7FFFFFFF;
-    expect("packed size", replayssm_prefill_packed(&l, &ls, (int64_t)1 << 31, dummy, 0, nullptr, w, w, w, w, w, 0, nullptr),
+    expect("packed size", replayssm_prefill_packed(&l, &ls, (int64_t)1 << 31, dummy, 0, nullptr, w, w, w, w, w, 0, nullptr, 0, nullptr),
            RSSM_E_ARG);
     l.n_heads = 8;
-    expect("packed huge", replayssm_prefill_packed(&l, &ls, INT64_MAX, dummy, 0, nullptr, w, w, w, w, w, 0, nullptr),
+    expect("packed huge", replayssm_prefill_packed(&l, &ls, INT64_MAX, dummy, 0, nullptr, w, w, w, w, w, 0, nullptr, 0, nullptr),
            RSSM_E_ARG);
-    expect("packed null", replayssm_prefill_packed(&l, &ls, 4, dummy, 0, nullptr, nullptr, w, w, w, w, 0, nullptr),
+    expect("packed null", replayssm_prefill_packed(&l, &ls, 4, dummy, 0, nullptr, nullptr, w, w, w, w, 0, nullptr, 0, nullptr),
            RSSM_E_ARG);
-    expect("packed none", replayssm_prefill_packed(&l, &ls, 0, nullptr, 0, nullptr, w, w, w, w, w, 0, nullptr), RSSM_OK);
+    expect("packed none", replayssm_prefill_packed(&l, &ls, 0, nullptr, 0, nullptr, w, w, w, w, w, 0, nullptr, 0, nullptr), RSSM_OK);
     expect("norm units", replayssm_gated_norm((int64_t)1 << 25, 16384, 16384, w, 0, w, 0, 16384, w, 0.f, 0, w, 0, nullptr),
            RSSM_E_ARG);
     expect("norm null", replayssm_gated_norm(1, 8, 1, w, 0, nullptr, 0, 8, w, 0.f, 0, w, 0, nullptr), RSSM_E_ARG);

@@ -246,7 +246,7 @@ def _check_scan(y, S, yr, Sr, ym, Sm, what):
     ref.assert_within(S, Sr, tol(Sr, Sm), what + " state")
 
 
-SCAN_LENGTHS = [[0, 1, 15, 16, 17, 0, 63, 64, 65], [200], [1], [129, 0, 3]]
+SCAN_LENGTHS = [[0, 1, 15, 16, 17, 0, 63, 64, 65], [200], [1], [129, 0, 3], [255, 256, 0, 257, 700], [1300]]
 
 
 @pytest.mark.parametrize("lens", SCAN_LENGTHS)

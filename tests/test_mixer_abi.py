@@ -92,12 +92,18 @@ def test_packed_prefill_refuses(rs, m):
     st = rs.RssmState(*([16] * 11))
     A = ctypes.addressof
     call = lambda total=8, cu=16, fz=0, x=16, C=16, y=16, yt=0: L.replayssm_prefill_packed(  # noqa: E731
-        A(d), A(st), total, cu, fz, None, x, 16, C, 16, y, yt, None)
+        A(d), A(st), total, cu, fz, None, x, 16, C, 16, y, yt, None, 0, None)
     assert call(total=-1) == -1 and call(total=1 << 29) == -1 and call(fz=3) == -1 and call(yt=2) == -2
     assert call(cu=None) == -1 and call(x=None) == -1 and call(C=None) == -1
-    assert L.replayssm_prefill_packed(None, A(st), 8, 16, 0, None, 16, 16, 16, 16, 16, 0, None) == -1
-    assert L.replayssm_prefill_packed(A(d), None, 8, 16, 0, None, 16, 16, 16, 16, 16, 0, None) == -1
+    assert L.replayssm_prefill_packed(None, A(st), 8, 16, 0, None, 16, 16, 16, 16, 16, 0, None, 0, None) == -1
+    assert L.replayssm_prefill_packed(A(d), None, 8, 16, 0, None, 16, 16, 16, 16, 16, 0, None, 0, None) == -1
     assert call(total=0, cu=None) == 0
+    ws = lambda n: L.replayssm_prefill_packed_workspace(A(d), n)  # noqa: E731
+    assert ws(-1) == 0 and ws(0) == 0 and ws(1 << 31) == 0 and ws(100000) > 0
+    assert L.replayssm_prefill_packed(A(d), A(st), 100000, 16, 0, None, 16, 16, 16, 16, 16, 0, 16, ws(100000) - 1,
+                                      None) == -1 and b"workspace" in L.replayssm_last_error()
+    f = rs._make_desc(4, 8, 64, 128, 1, 16, 1, rs.F32)
+    assert L.replayssm_prefill_packed_workspace(A(f), 100000) == 0
 
 
 def test_norms_refuse(m):
