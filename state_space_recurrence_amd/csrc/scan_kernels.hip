@@ -38,32 +38,34 @@ namespace {
 
 constexpr int kQ = kScanChunk;
 constexpr int kRowN = 136;   // elements of an LDS row of 128: 16 bytes more, so that 16 rows start in different banks
-constexpr int kRowQ = 72;    // elements of an LDS row of 64
+constexpr int kRowQ = 64;    // elements of an LDS row of 64, its 16-byte pieces exchanged by row (see piece)
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef unsigned int u2v __attribute__((ext_vector_type(2)));
 
 struct ScanSmem {
-    uint16_t B[kQ][kRowN];            // B_j[n], n exchanged
-    uint16_t C[kQ][kRowN];            // C_t[n], n exchanged
-    uint16_t BT[kN][kRowQ];           // B_j[n] as [n][j], j exchanged
-    uint16_t XT[kScanHeads][kP][kRowQ];   // x_j[p] as [p][j], j exchanged
-    float chi[4][kQ], clo[4][kQ];     // per wave: c_t / ln 2 as two floats
-    float dt[4][kQ];                  // dt_j
-    float cf[4][kQ];                  // dt_j exp(c_31 - c_j), j < 32
-    float w[4][kQ];                   // dt_j exp(c_63 - c_j)
-    int bad;                          // first token of the chunk with a non-finite x
+    alignas(16) uint16_t B[kQ][kRowN];    // B_j[n], n exchanged
+    alignas(16) uint16_t C[kQ][kRowN];    // C_t[n], n exchanged
+    alignas(16) uint16_t BT[kN][kRowQ];   // B_j[n] as [n][j], j exchanged
+    alignas(16) uint16_t XT[kScanHeads][kP][kRowQ];   // x_j[p] as [p][j], j exchanged
+    alignas(16) float chi[4][kQ];         // per wave: c_t / ln 2 as two floats
+    alignas(16) float clo[4][kQ];
+    alignas(16) float dt[4][kQ];          // dt_j
+    alignas(16) float cf[4][kQ];          // dt_j exp(c_31 - c_j), j < 32
+    alignas(16) float w[4][kQ];           // dt_j exp(c_63 - c_j)
+    int bad;                              // first token of the chunk with a non-finite x
 };
 
 // Position of quad q (4 elements) among the quads of a row: 1 and 2 of each four exchanged.
 __device__ __forceinline__ int quad_at(int q) { return (q & ~3) | ((q & 1) << 1) | ((q >> 1) & 1); }
 
-__device__ __forceinline__ b8v operand(const uint16_t *p) {
-    return __builtin_bit_cast(b8v, *reinterpret_cast<const u4v *>(p));
+__device__ __forceinline__ b8v operand(const void *p) {
+    return __builtin_bit_cast(b8v, *reinterpret_cast<const f4v *>(p));
 }
 
 typedef float f2v __attribute__((ext_vector_type(2)));
 typedef __bf16 b2v __attribute__((ext_vector_type(2)));
+typedef __bf16 b4v __attribute__((ext_vector_type(4)));
 
 // v = part[0] + part[1] + ... to 8 NP bits (each part one rounding, two values an instruction)
 template <int NP>
@@ -99,6 +101,16 @@ __device__ __forceinline__ f8v read8(const float *p) {   // p[0..3], p[8..11]
     return f8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
+// Rows of 64 elements are read 16 consecutive rows at a time (operands) and
+// written at every eighth row (transposed staging).  Piece k (16 bytes) of row
+// n is kept at k ^ turn(n): both then spread over the banks.  turn(n + 32 m) =
+// turn(n) ^ 2 m and, for n a multiple of 8, turn(n + i) = turn(n) ^ (i / 2), so
+// an address is one of four lane values plus a constant.
+__device__ __forceinline__ int turn(int n) { return ((n >> 1) ^ (n >> 4)) & 7; }
+
+// Byte offset of piece k of row n.
+__device__ __forceinline__ int piece_offset(int n, int k) { return 2 * kRowQ * n + 16 * (k ^ turn(n)); }
+
 // Column i of four rows of eight 16-bit values.
 template <int I>
 __device__ __forceinline__ u2v column(u4v a, u4v b, u4v c, u4v d) {
@@ -106,11 +118,12 @@ __device__ __forceinline__ u2v column(u4v a, u4v b, u4v c, u4v d) {
     return u2v{__builtin_amdgcn_perm(b[I / 2], a[I / 2], sel), __builtin_amdgcn_perm(d[I / 2], c[I / 2], sel)};
 }
 
-// The four rows' columns 0..7 to LDS rows p, p + kRowQ, ...
+// The four rows' columns 0..7 to LDS rows n .. n + 7; `off` is the offset of
+// row n with the quad's position in it.
 template <int I = 0>
-__device__ __forceinline__ void store_columns(uint16_t *p, u4v a, u4v b, u4v c, u4v d) {
-    *reinterpret_cast<u2v *>(p + I * kRowQ) = column<I>(a, b, c, d);
-    if constexpr (I < 7) store_columns<I + 1>(p, a, b, c, d);
+__device__ __forceinline__ void store_columns(char *m, int off, u4v a, u4v b, u4v c, u4v d) {
+    *reinterpret_cast<u2v *>(m + (off ^ (16 * (I / 2))) + 2 * kRowQ * I) = column<I>(a, b, c, d);
+    if constexpr (I < 7) store_columns<I + 1>(m, off, a, b, c, d);
 }
 
 // A state tile from and to memory: values 4 i .. 4 i + 3 at s + 8 i.
@@ -131,13 +144,36 @@ __device__ __forceinline__ void put_tile(const f16v &v, float *s) {
         *reinterpret_cast<float4 *>(s + 8 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
-// Inclusive sum over lanes 0..l.
-__device__ __forceinline__ double prefix(double v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const double o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_d(double v) {   // lanes without a source get 0
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ double lane_d(double v, int l) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)u, l), hi = __builtin_amdgcn_readlane((int)(u >> 32), l);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Inclusive sum over lanes 0..l: shifts within rows of 16, then the last lane
+// of a row into the next one, and lane 31 into the upper half.
+__device__ __forceinline__ double prefix(double v) {
+    v += dpp_d<0x111, 0xF>(v);
+    v += dpp_d<0x112, 0xF>(v);
+    v += dpp_d<0x114, 0xF>(v);
+    v += dpp_d<0x118, 0xF>(v);
+    v += dpp_d<0x142, 0xA>(v);
+    v += dpp_d<0x143, 0xC>(v);
+    return v;
+}
+
+// An address part that is derived again in every chunk instead of being held
+// in a register each (the accumulators need them).
+__device__ __forceinline__ int recomputed(int v) {
+    asm volatile("" : "+v"(v));
     return v;
 }
 
@@ -180,7 +216,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
     const int entry = pair / r.G, g = pair - entry * r.G;
 
     const int seq = __builtin_amdgcn_readfirstlane(segment_owner(a, entry, lane));
-    const int start = r.cu[seq], end = r.cu[seq + 1];
+    const int start = __builtin_amdgcn_readfirstlane(r.cu[seq]), end = __builtin_amdgcn_readfirstlane(r.cu[seq + 1]);
     if (start < 0 || end > r.total || end <= start) return;
     const int k = entry - (start / a.lseg + seq);
     if (k < 0 || (int64_t)k * a.lseg >= end - start) return;
@@ -188,7 +224,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
     const int len = end - tok0 < a.lseg ? end - tok0 : a.lseg;
     const bool last = tok0 + len == end;
     if (LOCAL && last) return;
-    const int b = slot_of_row(r, seq);
+    const int b = __builtin_amdgcn_readfirstlane(slot_of_row(r, seq));
     if (b < 0) return;   // padding row
 
     const int hh = wave >> 1;                  // the wave's head among the workgroup's
@@ -238,7 +274,8 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
     const uint16_t *Bin = reinterpret_cast<const uint16_t *>(r.Bm) + (size_t)tok0 * GN + (size_t)g * kN;
     const uint16_t *Cin = reinterpret_cast<const uint16_t *>(r.Cm) + (size_t)tok0 * GN + (size_t)g * kN;
     const uint16_t *dtin = reinterpret_cast<const uint16_t *>(r.dt) + (size_t)tok0 * r.H + h;
-    TY *yout = reinterpret_cast<TY *>(r.y) + (size_t)tok0 * HP + (size_t)h * kP + p0 + 4 * hf;
+    TY *yout = reinterpret_cast<TY *>(r.y) + (size_t)tok0 * HP + (size_t)h * kP + p0;
+    const int yoff = (c * (int)HP + 4 * hf) * (int)sizeof(TY);
     const double A2 = (double)r.A[h] * 1.4426950408889634;
     const float Dh = r.D[h];
 
@@ -249,38 +286,38 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
     const size_t xcol = (size_t)(g * hpg + (xhl < hpg ? xhl : hpg - 1)) * kP + 8 * xo;
     u4v rB[4], rC[4], rX[4];
     float rdt;
-    // Lane offsets (bytes) from the chunk's first row, which is uniform: a
-    // chunk spans less than 4 GiB, so 32 bits do.
-    const unsigned bpitch = (unsigned)GN * 2, xpitch = (unsigned)HP * 2;
-    const unsigned boff = 16 * bo, xoff = (unsigned)xcol * 2;
-    auto fetch = [&](int t0) {   // chunk at t0; tokens past the segment are zeros
-        const int rem = len - t0;
-        const char *bp = reinterpret_cast<const char *>(Bin + (size_t)t0 * GN);
-        const char *cp = reinterpret_cast<const char *>(Cin + (size_t)t0 * GN);
-        const char *xp = reinterpret_cast<const char *>(xin + (size_t)t0 * HP);
-        if (rem >= kQ) {
-            const unsigned bv = boff + 4 * bq * bpitch, xv = xoff + 4 * xq * xpitch;
+    // Buffer loads: the chunk's first row is the (uniform) base, and rows past
+    // the segment fall outside the resource and read as zeros.
+    const int bpitch = (int)GN * 2, xpitch = (int)HP * 2;
+    const int boff = 16 * bo + 4 * bq * bpitch, xoff = (int)xcol * 2 + 4 * xq * xpitch, doff = 2 * lane * r.H;
+    auto fetch = [&](int t0) {
+        const int left = len - t0 < 0 ? 0 : (len - t0 < kQ ? len - t0 : kQ);
+        const int rem = __builtin_amdgcn_readfirstlane(left);   // (a vector clamp would make the resources vector values)
+        const int bv = recomputed(boff), xv = recomputed(xoff);
+        const auto bs = uniform_rsrc(Bin + (size_t)t0 * GN, rem * bpitch);
+        const auto xs = uniform_rsrc(xin + (size_t)t0 * HP, rem * xpitch);
+        const auto ds = uniform_rsrc(dtin + (size_t)t0 * r.H, rem * 2 * r.H);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                rB[i] = *reinterpret_cast<const u4v *>(bp + i * bpitch + bv);
-                if (OUT) rC[i] = *reinterpret_cast<const u4v *>(cp + i * bpitch + bv);
-                rX[i] = *reinterpret_cast<const u4v *>(xp + i * xpitch + xv);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int tb = 4 * bq + i, tx = 4 * xq + i;
-                rB[i] = rX[i] = (u4v)0u;
-                if (OUT) rC[i] = (u4v)0u;
-                if (tb < rem) {
-                    rB[i] = *reinterpret_cast<const u4v *>(bp + (boff + tb * bpitch));
-                    if (OUT) rC[i] = *reinterpret_cast<const u4v *>(cp + (boff + tb * bpitch));
-                }
-                if (tx < rem) rX[i] = *reinterpret_cast<const u4v *>(xp + (xoff + tx * xpitch));
-            }
+        for (int i = 0; i < 4; ++i) {
+            rB[i] = __builtin_amdgcn_raw_buffer_load_b128(bs, bv + i * bpitch, 0, 0);
+            rX[i] = __builtin_amdgcn_raw_buffer_load_b128(xs, xv + i * xpitch, 0, 0);
         }
-        rdt = lane < rem ? vec8<uint16_t>::get(dtin + (size_t)t0 * r.H + (unsigned)(lane * r.H)) : 0.f;
+        if (OUT) {
+            const auto cs = uniform_rsrc(Cin + (size_t)t0 * GN, rem * bpitch);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rC[i] = __builtin_amdgcn_raw_buffer_load_b128(cs, bv + i * bpitch, 0, 0);
+        }
+        rdt = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ds, doff, 0, 0) << 16);
     };
+
+    // LDS offsets of the staging and of the operands
+    const int at_b = quad_at(bq), at_x = quad_at(xq);
+    const int put_b0 = piece_offset(8 * bo, at_b >> 1) + 8 * (at_b & 1);
+    const int put_x0 = (int)sizeof(sm.XT[0]) * xh + piece_offset(8 * xo, at_x >> 1) + 8 * (at_x & 1);
+    const int put_r = 2 * kRowN * 4 * bq + 8 * quad_at(2 * bo);
+    const int get_x0 = (int)sizeof(sm.XT[0]) * hh + piece_offset(p0 + c, hf);
+    const int get_b0 = piece_offset(c, hf);
+    const int get_r = 2 * kRowN * c + 16 * hf;
 
     double total = 0.0;   // decay of the segment (LOCAL)
     fetch(0);
@@ -288,18 +325,19 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
         __syncthreads();   // the previous chunk's LDS reads are done
         if (threadIdx.x == 0) sm.bad = kQ;
         {
-            store_columns(&sm.BT[8 * bo][4 * quad_at(bq)], rB[0], rB[1], rB[2], rB[3]);
-            if (OUT) {
+            const int put_b = recomputed(put_b0), put_x = recomputed(put_x0);
+            store_columns(reinterpret_cast<char *>(sm.BT), put_b, rB[0], rB[1], rB[2], rB[3]);
+            if (OUT) {   // quads 2 bo and 2 bo + 1 of a row are two positions apart
+                char *pb = reinterpret_cast<char *>(sm.B) + put_r, *pc = reinterpret_cast<char *>(sm.C) + put_r;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int n0 = 4 * quad_at(2 * bo), n1 = 4 * quad_at(2 * bo + 1);
-                    *reinterpret_cast<u2v *>(&sm.B[4 * bq + i][n0]) = u2v{rB[i].x, rB[i].y};
-                    *reinterpret_cast<u2v *>(&sm.B[4 * bq + i][n1]) = u2v{rB[i].z, rB[i].w};
-                    *reinterpret_cast<u2v *>(&sm.C[4 * bq + i][n0]) = u2v{rC[i].x, rC[i].y};
-                    *reinterpret_cast<u2v *>(&sm.C[4 * bq + i][n1]) = u2v{rC[i].z, rC[i].w};
+                    *reinterpret_cast<u2v *>(pb + 2 * kRowN * i) = u2v{rB[i].x, rB[i].y};
+                    *reinterpret_cast<u2v *>(pb + 2 * kRowN * i + 16) = u2v{rB[i].z, rB[i].w};
+                    *reinterpret_cast<u2v *>(pc + 2 * kRowN * i) = u2v{rC[i].x, rC[i].y};
+                    *reinterpret_cast<u2v *>(pc + 2 * kRowN * i + 16) = u2v{rC[i].z, rC[i].w};
                 }
             }
-            store_columns(&sm.XT[xh][8 * xo][4 * quad_at(xq)], rX[0], rX[1], rX[2], rX[3]);
+            store_columns(reinterpret_cast<char *>(sm.XT), put_x, rX[0], rX[1], rX[2], rX[3]);
         }
         int q = len - t0 < kQ ? len - t0 : kQ;   // tokens of this chunk
         if (OUT) {
@@ -320,21 +358,21 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
         }
         __syncthreads();
         if (OUT) {
-            const int stop = sm.bad > 0 ? sm.bad : 1;
+            const int bad = __builtin_amdgcn_readfirstlane(sm.bad), stop = bad > 0 ? bad : 1;
             if (stop < q) {
                 q = stop;
-                for (int i = threadIdx.x; i < kScanHeads * kP * kQ; i += 256) {
-                    const int j = i & (kQ - 1), p = (i >> 6) & (kP - 1);
-                    if (j >= q) sm.XT[i >> 12][p][4 * quad_at(j >> 2) + (j & 3)] = 0;
-                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (4 * xq + i >= q) rX[i] = (u4v)0u;
+                store_columns(reinterpret_cast<char *>(sm.XT), recomputed(put_x0), rX[0], rX[1], rX[2], rX[3]);
                 if (lane >= q) rdt = 0.f;
                 __syncthreads();
             }
         }
 
         // ---- decays of the wave's head (both waves of a head compute them)
-        const double cum = prefix(A2 * (double)rdt, lane);
-        const double c31 = __shfl(cum, 31), c63 = __shfl(cum, 63);
+        const double cum = prefix(A2 * (double)rdt);
+        const double c31 = lane_d(cum, 31), c63 = lane_d(cum, 63);
         {
             const float hi = (float)cum;
             sm.chi[wave][lane] = hi;
@@ -346,8 +384,9 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
         const float lam = __builtin_amdgcn_exp2f((float)c63);
         total += c63;
         const int t1 = t0 + q;
+        const char *xt = reinterpret_cast<const char *>(sm.XT), *bt = reinterpret_cast<const char *>(sm.BT);
+        const int get_x = recomputed(get_x0), get_b = recomputed(get_b0);
         __builtin_amdgcn_wave_barrier();
-        if (!OUT && t1 < len) fetch(t1);
 
         if (OUT && live) {
             // ---- y^T[p][t] = sum_n S[p][n] C_t[n] and the Gram tiles G^T[j][t] = B_j . C_t
@@ -355,8 +394,9 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
             auto step = [&](const f16v &tile, int ks) {
                 b8v s[YP];
                 split<YP>(half_of(tile, ks & 1), s);
-                const b8v b0 = operand(&sm.B[c][16 * ks + 8 * hf]), b1 = operand(&sm.B[32 + c][16 * ks + 8 * hf]);
-                const b8v c0 = operand(&sm.C[c][16 * ks + 8 * hf]), c1 = operand(&sm.C[32 + c][16 * ks + 8 * hf]);
+                const char *pb = reinterpret_cast<const char *>(sm.B) + get_r + 32 * ks;
+                const char *pc = reinterpret_cast<const char *>(sm.C) + get_r + 32 * ks;
+                const b8v b0 = operand(pb), b1 = operand(pb + 64 * kRowN), c0 = operand(pc), c1 = operand(pc + 64 * kRowN);
                 g00 = mfma(b0, c0, g00);
                 g01 = mfma(b0, c1, g01);
                 g11 = mfma(b1, c1, g11);
@@ -374,8 +414,6 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
             step(st2, 5);
             step(st3, 6);
             step(st3, 7);
-            // the next chunk is requested here, when the state's parts are done with
-            if (t1 < len) fetch(t1);
             const float h0 = sm.chi[wave][c], l0 = sm.clo[wave][c];
             const float h1 = sm.chi[wave][32 + c], l1 = sm.clo[wave][32 + c];
             const float hm = sm.chi[wave][31], lm = sm.clo[wave][31];
@@ -398,9 +436,9 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int j = 16 * s + 4 * hf + 8 * (i >> 2) + (i & 3);
-                            const float e = __builtin_amdgcn_exp2f((ht - ch[i]) + (lt - cl[i]));
-                            m[i] = j <= c ? m[i] * (d[i] * e) : 0.f;
-                            m[i] += j == c ? Dh : 0.f;
+                            float e = m[i] * (d[i] * __builtin_amdgcn_exp2f((ht - ch[i]) + (lt - cl[i])));
+                            asm("" : "+v"(e));   // computed in every lane and selected, not branched around
+                            m[i] = j < c ? e : (j == c ? e + Dh : 0.f);
                         }
                     } else {
                         const f8v f = read8(&sm.cf[wave][j0]);
@@ -409,7 +447,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
                     }
                     b8v part[YP];
                     split<YP>(m, part);
-                    const b8v x = operand(&sm.XT[hh][p0 + c][32 * jt + 16 * s + 8 * hf]);
+                    const b8v x = operand(xt + (get_x ^ (64 * jt + 32 * s)));
 #pragma unroll
                     for (int i = YP - 1; i >= 0; --i) y = mfma(x, part[i], y);
                 }
@@ -417,27 +455,26 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
             apply(g00, 0, h0, l0, true, y0);
             apply(g01, 0, h1, l1, false, y1);
             apply(g11, 1, h1, l1, true, y1);
-            auto store = [&](const f16v &y, int t) {
-                if (t >= q) return;
-                TY *o = yout + (size_t)(t0 + t) * HP;
+            // rows past the chunk fall outside the resource
+            const auto ys = uniform_rsrc(yout + (size_t)t0 * HP, q * (int)HP * (int)sizeof(TY));
+            auto store = [&](const f16v &y, int off) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if constexpr (sizeof(TY) == 4) {
-                        *reinterpret_cast<float4 *>(o + 8 * i) =
-                            make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-                    } else {
-                        typedef float f4x __attribute__((ext_vector_type(4)));
-                        typedef __bf16 b4x __attribute__((ext_vector_type(4)));
-                        *reinterpret_cast<u2v *>(o + 8 * i) = __builtin_bit_cast(
-                            u2v, __builtin_convertvector(f4x{y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]}, b4x));
-                    }
+                    const f4v v = {y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]};
+                    const int at = off + 8 * i * (int)sizeof(TY);
+                    if constexpr (sizeof(TY) == 4)
+                        __builtin_amdgcn_raw_buffer_store_b128(v, ys, at, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b64(
+                            __builtin_bit_cast(u2v, __builtin_convertvector(v, b4v)), ys, at, 0, 0);
                 }
             };
-            store(y0, c);
-            store(y1, 32 + c);
-        } else if (OUT && t1 < len) {
-            fetch(t1);
+            store(y0, yoff);
+            store(y1, yoff + 32 * (int)HP * (int)sizeof(TY));
         }
+        // The next chunk is requested here, when only the state is held.
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(t1);
 
         // ---- S^T[n][p] = exp(c_63) S^T + sum_j B_j[n] (w_j x_j[p])
 #pragma unroll
@@ -449,15 +486,15 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
         }
 #pragma unroll
         for (int js = 0; js < 4; ++js) {
-            f8v v = vec8<uint16_t>::widen(*reinterpret_cast<const u4v *>(&sm.XT[hh][p0 + c][16 * js + 8 * hf]));
+            f8v v = vec8<uint16_t>::widen(*reinterpret_cast<const u4v *>(__builtin_assume_aligned(xt + (get_x ^ (32 * js)), 16)));
             const f8v w = read8(&sm.w[wave][16 * js + 4 * hf]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= w[i];
             b8v part[3];
             split<3>(v, part);
-            const uint16_t *bt = &sm.BT[c][16 * js + 8 * hf];
-            const b8v b0 = operand(bt), b1 = operand(bt + 32 * kRowQ), b2 = operand(bt + 64 * kRowQ),
-                      b3 = operand(bt + 96 * kRowQ);
+            const b8v b0 = operand(bt + (get_b ^ (32 * js))), b1 = operand(bt + (get_b ^ (32 * (js ^ 1))) + 64 * kRowQ),
+                      b2 = operand(bt + (get_b ^ (32 * (js ^ 2))) + 128 * kRowQ),
+                      b3 = operand(bt + (get_b ^ (32 * (js ^ 3))) + 192 * kRowQ);
 #pragma unroll
             for (int i = 2; i >= 0; --i) {
                 st0 = mfma(b0, part[i], st0);
