@@ -48,12 +48,12 @@ struct ScanSmem {
     alignas(16) uint16_t C[kQ][kRowN];    // C_t[n], n exchanged
     alignas(16) uint16_t BT[kN][kRowQ];   // B_j[n] as [n][j], j exchanged
     alignas(16) uint16_t XT[kScanHeads][kP][kRowQ];   // x_j[p] as [p][j], j exchanged
-    alignas(16) float chi[4][kQ];         // per wave: c_t / ln 2 as two floats
-    alignas(16) float clo[4][kQ];
-    alignas(16) float dt[4][kQ];          // dt_j
-    alignas(16) float cf[4][kQ];          // dt_j exp(c_31 - c_j), j < 32
+    // per wave, with c_t / ln 2 = k_t + f_t, k_t whole and 0 <= f_t < 1:
+    alignas(16) int k[4][kQ];
+    alignas(16) float cf[4][kQ];          // dt_j 2^-f_j
     alignas(16) float w[4][kQ];           // dt_j exp(c_63 - c_j)
-    int bad;                              // first token of the chunk with a non-finite x
+    float rf[4][kQ], ri[4][kQ];           // 2^f_t, 2^-f_t
+    int bad[2];                           // first token with a non-finite x, of even and odd chunks
 };
 
 // Position of quad q (4 elements) among the quads of a row: 1 and 2 of each four exchanged.
@@ -96,7 +96,15 @@ __device__ __forceinline__ f8v half_of(const f16v &v, int s) {
     return r;
 }
 
-__device__ __forceinline__ f8v read8(const float *p) {   // p[0..3], p[8..11]
+typedef int i8v __attribute__((ext_vector_type(8)));
+typedef int i4v __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ i8v read8(const int *p) {   // p[0..3], p[8..11]
+    const i4v a = *reinterpret_cast<const i4v *>(p), b = *reinterpret_cast<const i4v *>(p + 8);
+    return i8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
+__device__ __forceinline__ f8v read8(const float *p) {
     const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 8);
     return f8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
@@ -229,7 +237,7 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
 
     const int hh = wave >> 1;                  // the wave's head among the workgroup's
     const int hl = hblk * kScanHeads + hh;     // ... within the group
-    const bool live = hl < hpg;                // an odd head count leaves half a workgroup idle
+    const bool live = hl < hpg;                // an odd head count: half a workgroup runs the last head again, unseen
     const int h = g * hpg + (live ? hl : hpg - 1);
     const int p0 = (wave & 1) * 32;            // the wave's state rows
     const size_t HP = (size_t)r.H * kP, GN = (size_t)r.G * kN;
@@ -321,9 +329,10 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
 
     double total = 0.0;   // decay of the segment (LOCAL)
     fetch(0);
-    for (int t0 = 0; t0 < len;) {
+    int odd = 0;
+    if (threadIdx.x < 2) sm.bad[threadIdx.x] = kQ;
+    for (int t0 = 0; t0 < len; odd ^= 1) {
         __syncthreads();   // the previous chunk's LDS reads are done
-        if (threadIdx.x == 0) sm.bad = kQ;
         {
             const int put_b = recomputed(put_b0), put_x = recomputed(put_x0);
             store_columns(reinterpret_cast<char *>(sm.BT), put_b, rB[0], rB[1], rB[2], rB[3]);
@@ -343,7 +352,6 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
         if (OUT) {
             // M_tj = 0 for j > t does not keep a non-finite x_j out of y_t: a
             // chunk ends before a token that holds one, which is then taken alone.
-            __syncthreads();
             unsigned seen = 0;
             int first = kQ;
 #pragma unroll
@@ -354,11 +362,12 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
                 if (bits & 0x80008000u) first = 4 * xq + i;
                 seen |= bits;
             }
-            if (seen & 0x80008000u) atomicMin(&sm.bad, first);
+            if (seen & 0x80008000u) atomicMin(&sm.bad[odd], first);
         }
         __syncthreads();
         if (OUT) {
-            const int bad = __builtin_amdgcn_readfirstlane(sm.bad), stop = bad > 0 ? bad : 1;
+            const int bad = __builtin_amdgcn_readfirstlane(sm.bad[odd]), stop = bad > 0 ? bad : 1;
+            if (threadIdx.x == 0) sm.bad[odd ^ 1] = kQ;   // read in the last chunk, set in the next
             if (stop < q) {
                 q = stop;
 #pragma unroll
@@ -370,25 +379,30 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
             }
         }
 
-        // ---- decays of the wave's head (both waves of a head compute them)
-        const double cum = prefix(A2 * (double)rdt);
-        const double c31 = lane_d(cum, 31), c63 = lane_d(cum, 63);
-        {
-            const float hi = (float)cum;
-            sm.chi[wave][lane] = hi;
-            sm.clo[wave][lane] = (float)(cum - (double)hi);
-            sm.dt[wave][lane] = rdt;
-            sm.cf[wave][lane] = lane < 32 ? rdt * __builtin_amdgcn_exp2f((float)(c31 - cum)) : 0.f;
-            sm.w[wave][lane] = rdt * __builtin_amdgcn_exp2f((float)(c63 - cum));
-        }
-        const float lam = __builtin_amdgcn_exp2f((float)c63);
-        total += c63;
         const int t1 = t0 + q;
         const char *xt = reinterpret_cast<const char *>(sm.XT), *bt = reinterpret_cast<const char *>(sm.BT);
         const int get_x = recomputed(get_x0), get_b = recomputed(get_b0);
-        __builtin_amdgcn_wave_barrier();
 
-        if (OUT && live) {
+        // ---- decays of the wave's head (both waves of a head compute them).
+        // exp(c_t - c_j) = 2^(k_t - k_j) 2^f_t 2^-f_j: the fractions' powers
+        // are taken once per token, the whole part moves an exponent exactly.
+        float lam;
+        auto decays = [&]() {
+            const double cum = prefix(A2 * (double)rdt), whole = __builtin_floor(cum);
+            const double c63 = lane_d(cum, 63);
+            const float f = (float)(cum - whole), ri = __builtin_amdgcn_exp2f(-f);
+            sm.k[wave][lane] = (int)whole;
+            sm.cf[wave][lane] = rdt * ri;
+            sm.w[wave][lane] = rdt * __builtin_amdgcn_exp2f((float)(c63 - cum));
+            sm.rf[wave][lane] = __builtin_amdgcn_exp2f(f);
+            sm.ri[wave][lane] = ri;
+            lam = __builtin_amdgcn_exp2f((float)c63);
+            total += c63;
+            __builtin_amdgcn_wave_barrier();
+        };
+        if (!OUT) decays();
+
+        if (OUT) {
             // ---- y^T[p][t] = sum_n S[p][n] C_t[n] and the Gram tiles G^T[j][t] = B_j . C_t
             f16v y0 = (f16v)0.f, y1 = (f16v)0.f, g00 = (f16v)0.f, g01 = (f16v)0.f, g11 = (f16v)0.f;
             auto step = [&](const f16v &tile, int ks) {
@@ -414,36 +428,30 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
             step(st2, 5);
             step(st3, 6);
             step(st3, 7);
-            const float h0 = sm.chi[wave][c], l0 = sm.clo[wave][c];
-            const float h1 = sm.chi[wave][32 + c], l1 = sm.clo[wave][32 + c];
-            const float hm = sm.chi[wave][31], lm = sm.clo[wave][31];
-            const float e0 = __builtin_amdgcn_exp2f(h0 + l0), e1 = __builtin_amdgcn_exp2f(h1 + l1);
-            const float rf = __builtin_amdgcn_exp2f((h1 - hm) + (l1 - lm));   // exp(c_t - c_31)
+            decays();
+            const int k0 = sm.k[wave][c], k1 = sm.k[wave][32 + c];
+            const float r0 = sm.rf[wave][c], r1 = sm.rf[wave][32 + c];
+            const float D0 = Dh * sm.ri[wave][c], D1 = Dh * sm.ri[wave][32 + c];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                y0[i] *= e0;
-                y1[i] *= e1;
+                y0[i] = __builtin_ldexpf(y0[i], k0);
+                y1[i] = __builtin_ldexpf(y1[i], k1);
             }
-            // ---- y^T += x^T M^T, M^T as the operand straight from the Gram accumulators
-            auto apply = [&](const f16v &gram, int jt, float ht, float lt, bool diag, f16v &y) {
+            // ---- y^T += x^T M^T without the factor 2^f_t, M^T as the operand straight from the Gram accumulators
+            auto apply = [&](const f16v &gram, int jt, int kt, float Dt, bool diag, f16v &y) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     const int j0 = 32 * jt + 16 * s + 4 * hf;
                     f8v m = half_of(gram, s);
-                    if (diag) {
-                        const f8v ch = read8(&sm.chi[wave][j0]), cl = read8(&sm.clo[wave][j0]);
-                        const f8v d = read8(&sm.dt[wave][j0]);
+                    const f8v cf = read8(&sm.cf[wave][j0]);
+                    const i8v kj = read8(&sm.k[wave][j0]);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 8; ++i) {
+                        m[i] = __builtin_ldexpf(m[i] * cf[i], kt - kj[i]);
+                        if (diag) {
                             const int j = 16 * s + 4 * hf + 8 * (i >> 2) + (i & 3);
-                            float e = m[i] * (d[i] * __builtin_amdgcn_exp2f((ht - ch[i]) + (lt - cl[i])));
-                            asm("" : "+v"(e));   // computed in every lane and selected, not branched around
-                            m[i] = j < c ? e : (j == c ? e + Dh : 0.f);
+                            m[i] = j < c ? m[i] : (j == c ? m[i] + Dt : 0.f);
                         }
-                    } else {
-                        const f8v f = read8(&sm.cf[wave][j0]);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) m[i] *= f[i] * rf;
                     }
                     b8v part[YP];
                     split<YP>(m, part);
@@ -452,11 +460,16 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
                     for (int i = YP - 1; i >= 0; --i) y = mfma(x, part[i], y);
                 }
             };
-            apply(g00, 0, h0, l0, true, y0);
-            apply(g01, 0, h1, l1, false, y1);
-            apply(g11, 1, h1, l1, true, y1);
-            // rows past the chunk fall outside the resource
-            const auto ys = uniform_rsrc(yout + (size_t)t0 * HP, q * (int)HP * (int)sizeof(TY));
+            apply(g00, 0, k0, D0, true, y0);
+            apply(g01, 0, k1, 0.f, false, y1);
+            apply(g11, 1, k1, D1, true, y1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                y0[i] *= r0;
+                y1[i] *= r1;
+            }
+            // rows past the chunk (and an unseen head's) fall outside the resource
+            const auto ys = uniform_rsrc(yout + (size_t)t0 * HP, live ? q * (int)HP * (int)sizeof(TY) : 0);
             auto store = [&](const f16v &y, int off) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
