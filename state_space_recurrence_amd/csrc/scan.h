@@ -9,7 +9,10 @@
 namespace rssm {
 
 constexpr int kScanChunk = 64;       // tokens per chunk
-constexpr int kScanHeads = 2;        // heads per workgroup (of one B/C group)
+
+// Heads per workgroup (of one B/C group): B and C are staged once for all of
+// them, and two chunks of four heads fill the LDS of a compute unit.
+inline int scan_heads(int hpg) { return hpg >= 3 ? 4 : hpg; }
 
 struct ScanParams {
     ReplayParams r;
@@ -22,12 +25,14 @@ struct ScanParams {
     int hb;            // workgroups per (segment, group)
 };
 
-// Tokens per segment for a call: long sequences are cut so that the card's
-// compute units all have work.
+// Tokens per segment for a call: long sequences are cut so that each of the
+// 256 compute units has a workgroup, and no finer.
 inline int scan_segment(int64_t total, int H, int G) {
-    const int64_t hb = (int64_t)G * ((H / G + kScanHeads - 1) / kScanHeads);
+    const int nh = scan_heads(H / G);
+    const int64_t hb = (int64_t)G * ((H / G + nh - 1) / nh);
     const int64_t chunks = (total + kScanChunk - 1) / kScanChunk;
-    int64_t per = (chunks * hb + 511) / 512;   // chunks per workgroup with two workgroups on every CU
+    const int64_t pieces = hb < 256 ? 256 / hb : 1;   // segments side by side
+    int64_t per = (chunks + pieces - 1) / pieces;
     if (per < 4) per = 4;
     return (int)(per * kScanChunk);
 }

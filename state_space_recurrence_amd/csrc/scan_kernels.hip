@@ -3,25 +3,33 @@
 //
 // A sequence is taken in chunks of 64 tokens.  With l_i = A dt_i, c_t the sum
 // of l over the chunk up to t, and S the state before the chunk:
-//     M_tj = (C_t . B_j) dt_j exp(c_t - c_j)  for j <= t, plus D at j = t
-//     y_t  = sum_j M_tj x_j + exp(c_t) S C_t
+//     M_tj = (C_t . B_j) dt_j exp(c_t - c_j)  for j <= t, else 0
+//     y_t  = sum_j M_tj x_j + exp(c_t) S C_t + D x_t
 //     S'   = exp(c_63) S + sum_j dt_j exp(c_63 - c_j) x_j (outer) B_j
 // One wave owns 32 of the 64 state rows p of a head and keeps its half of the
 // state, transposed [n][p], in the accumulators of v_mfma_f32_32x32x16_bf16
 // for the whole segment.  An accumulator holds 4 consecutive rows per lane
-// half, a matrix operand 8; the products' inner index may run in any order, so
-// every operand in LDS is stored with quads 1 and 2 of each 16 exchanged and
-// accumulators (the state for S C, the decayed Gram tile for M x) feed the
-// next product straight from registers.
+// half, an operand 8 consecutive inner indices; which n or p a row stands for,
+// and the order of the inner index, are free as long as both sides agree, so
+// accumulators (the state for S C, the decayed Gram tile for M x) are the next
+// product's operands straight from registers.
+//
+// Staging.  The chunk's B, C and x go from memory to LDS directly (16 bytes a
+// lane, no registers), one chunk ahead in the other of two buffers; rows of B
+// and C serve as operands of S C and of the Gram tiles as they lie, and the
+// transposed operands (B as [n][j], x as [p][j]) come from the same rows by
+// transposing LDS reads (4 rows x 16 columns a quarter wave).  Pairs of
+// 16-byte pieces are exchanged by row so that both kinds of reads spread over
+// the banks.
 //
 // Precision.  x, B, C are bf16 and exact operands.  Values formed in fp32
 // (state, M, weighted x) are split into bf16 parts, v = hi + mid + lo, and
 // multiplied part by part into the same fp32 accumulator: three parts carry
 // all 24 bits, two carry 16.  The state always uses three, so it is as exact
 // as an fp32 update; y uses three for fp32 outputs and two for bf16 ones,
-// whose own rounding is 2^-8.  Decay sums run in fp64 and are kept as two
-// floats: a difference of two long sums would otherwise lose the bits of a
-// short one.
+// whose own rounding is 2^-8.  Decay sums run in fp64 and are kept as a whole
+// and a fractional power of two: a difference of two long sums would
+// otherwise lose the bits of a short one.
 //
 // Long sequences.  When sequences x heads do not fill the card, a sequence is
 // cut into segments: a first launch leaves each segment's end state (the first
@@ -33,39 +41,54 @@
 #include "replay_common.h"
 #include "scan.h"
 
+#include <type_traits>
+
 namespace rssm {
 namespace {
 
 constexpr int kQ = kScanChunk;
-constexpr int kRowN = 136;   // elements of an LDS row of 128: 16 bytes more, so that 16 rows start in different banks
-constexpr int kRowQ = 64;    // elements of an LDS row of 64, its 16-byte pieces exchanged by row (see piece)
 
 typedef float f16v __attribute__((ext_vector_type(16)));
-typedef unsigned int u2v __attribute__((ext_vector_type(2)));
+typedef float f2v __attribute__((ext_vector_type(2)));
+typedef int i8v __attribute__((ext_vector_type(8)));
+typedef int i4v __attribute__((ext_vector_type(4)));
+typedef short s4v __attribute__((ext_vector_type(4)));
+typedef short s8v __attribute__((ext_vector_type(8)));
+typedef __bf16 b2v __attribute__((ext_vector_type(2)));
 
+// NH heads and 2 NH waves a workgroup.
+template <int NH>
 struct ScanSmem {
-    alignas(16) uint16_t B[kQ][kRowN];    // B_j[n], n exchanged
-    alignas(16) uint16_t C[kQ][kRowN];    // C_t[n], n exchanged
-    alignas(16) uint16_t BT[kN][kRowQ];   // B_j[n] as [n][j], j exchanged
-    alignas(16) uint16_t XT[kScanHeads][kP][kRowQ];   // x_j[p] as [p][j], j exchanged
+    struct Chunk {
+        alignas(16) char B[kQ][2 * kN];       // B_j[n]: 32-byte pair k of row j at k ^ (j mod 8)
+        alignas(16) char C[kQ][2 * kN];       // C_t[n], the same
+        alignas(16) char x[NH][kQ][2 * kP];   // x_j[p]: pair k of row j at k ^ (j / 2 mod 4)
+    } chunk[2];
     // per wave, with c_t / ln 2 = k_t + f_t, k_t whole and 0 <= f_t < 1:
-    alignas(16) int k[4][kQ];
-    alignas(16) float cf[4][kQ];          // dt_j 2^-f_j
-    alignas(16) float w[4][kQ];           // dt_j exp(c_63 - c_j)
-    float rf[4][kQ], ri[4][kQ];           // 2^f_t, 2^-f_t
-    int bad[2];                           // first token with a non-finite x, of even and odd chunks
+    alignas(16) int k[2 * NH][kQ];
+    alignas(16) float cf[2 * NH][kQ];         // dt_j 2^-f_j
+    alignas(16) float w[2 * NH][kQ];          // dt_j exp(c_63 - c_j)
+    float rf[2 * NH][kQ];                     // 2^f_t
 };
 
-// Position of quad q (4 elements) among the quads of a row: 1 and 2 of each four exchanged.
-__device__ __forceinline__ int quad_at(int q) { return (q & ~3) | ((q & 1) << 1) | ((q >> 1) & 1); }
+// Of each four quads the middle two trade places: row r of a 16-row tile
+// stands for element 4 swapped(r / 4) + r mod 4, which gives the rows of a lane
+// half (4 h .. 4 h + 3 and 8 + 4 h ..) eight consecutive elements.
+__device__ __forceinline__ int swapped(int q) { return (q & 1) << 1 | q >> 1; }
 
-__device__ __forceinline__ b8v operand(const void *p) {
+__device__ __forceinline__ b8v operand(const char *p) {
     return __builtin_bit_cast(b8v, *reinterpret_cast<const f4v *>(p));
 }
 
-typedef float f2v __attribute__((ext_vector_type(2)));
-typedef __bf16 b2v __attribute__((ext_vector_type(2)));
-typedef __bf16 b4v __attribute__((ext_vector_type(4)));
+// Eight inner indices (rows j .. j + 3 and j + 8 .. j + 11, STEP bytes a row)
+// of a transposed operand.
+template <int STEP>
+__device__ __forceinline__ b8v operand_t(const char *p) {
+    typedef __attribute__((address_space(3))) s4v lds_s4;
+    const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p);
+    const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + 8 * STEP));
+    return __builtin_bit_cast(b8v, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
 
 // v = part[0] + part[1] + ... to 8 NP bits (each part one rounding, two values an instruction)
 template <int NP>
@@ -96,49 +119,21 @@ __device__ __forceinline__ f8v half_of(const f16v &v, int s) {
     return r;
 }
 
-typedef int i8v __attribute__((ext_vector_type(8)));
-typedef int i4v __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ i8v read8(const int *p) {   // p[0..3], p[8..11]
-    const i4v a = *reinterpret_cast<const i4v *>(p), b = *reinterpret_cast<const i4v *>(p + 8);
-    return i8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-}
-
-__device__ __forceinline__ f8v read8(const float *p) {
+__device__ __forceinline__ f8v read8(const float *p) {   // p[0..3], p[8..11]
     const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 8);
     return f8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
-// Rows of 64 elements are read 16 consecutive rows at a time (operands) and
-// written at every eighth row (transposed staging).  Piece k (16 bytes) of row
-// n is kept at k ^ turn(n): both then spread over the banks.  turn(n + 32 m) =
-// turn(n) ^ 2 m and, for n a multiple of 8, turn(n + i) = turn(n) ^ (i / 2), so
-// an address is one of four lane values plus a constant.
-__device__ __forceinline__ int turn(int n) { return ((n >> 1) ^ (n >> 4)) & 7; }
-
-// Byte offset of piece k of row n.
-__device__ __forceinline__ int piece_offset(int n, int k) { return 2 * kRowQ * n + 16 * (k ^ turn(n)); }
-
-// Column i of four rows of eight 16-bit values.
-template <int I>
-__device__ __forceinline__ u2v column(u4v a, u4v b, u4v c, u4v d) {
-    constexpr unsigned sel = I & 1 ? 0x07060302 : 0x05040100;
-    return u2v{__builtin_amdgcn_perm(b[I / 2], a[I / 2], sel), __builtin_amdgcn_perm(d[I / 2], c[I / 2], sel)};
+__device__ __forceinline__ i8v read8(const int *p) {
+    const i4v a = *reinterpret_cast<const i4v *>(p), b = *reinterpret_cast<const i4v *>(p + 8);
+    return i8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
-// The four rows' columns 0..7 to LDS rows n .. n + 7; `off` is the offset of
-// row n with the quad's position in it.
-template <int I = 0>
-__device__ __forceinline__ void store_columns(char *m, int off, u4v a, u4v b, u4v c, u4v d) {
-    *reinterpret_cast<u2v *>(m + (off ^ (16 * (I / 2))) + 2 * kRowQ * I) = column<I>(a, b, c, d);
-    if constexpr (I < 7) store_columns<I + 1>(m, off, a, b, c, d);
-}
-
-// A state tile from and to memory: values 4 i .. 4 i + 3 at s + 8 i.
+// A state tile from and to memory: values 0..7 at s, 8..15 at s + 16.
 __device__ __forceinline__ void add_tile(f16v &v, const float *s, float f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float4 u = *reinterpret_cast<const float4 *>(s + 8 * i);
+        const float4 u = *reinterpret_cast<const float4 *>(s + 4 * i + 8 * (i >> 1));
         v[4 * i] += f * u.x;
         v[4 * i + 1] += f * u.y;
         v[4 * i + 2] += f * u.z;
@@ -149,7 +144,8 @@ __device__ __forceinline__ void add_tile(f16v &v, const float *s, float f) {
 __device__ __forceinline__ void put_tile(const f16v &v, float *s) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4 *>(s + 8 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        *reinterpret_cast<float4 *>(s + 4 * i + 8 * (i >> 1)) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
 template <int CTRL, int ROWS>
@@ -178,11 +174,22 @@ __device__ __forceinline__ double prefix(double v) {
     return v;
 }
 
-// An address part that is derived again in every chunk instead of being held
-// in a register each (the accumulators need them).
-__device__ __forceinline__ int recomputed(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
+// The lane number, opaque to the compiler: what is derived from it inside the
+// chunk loop is derived again in every chunk and held in no register between
+// (the accumulators need them all).
+__device__ __forceinline__ int lane_again() {
+    int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    asm volatile("" : "+v"(l));
+    return l;
+}
+
+// Exponent all ones in either half of any of the operand's dwords.
+__device__ __forceinline__ bool non_finite(b8v v) {
+    const u4v u = __builtin_bit_cast(u4v, v);
+    unsigned bits = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bits |= (u[i] & 0x7F807F80u) + 0x00800080u;
+    return (bits & 0x80008000u) != 0;
 }
 
 // Last sequence s whose first segment entry, cu[s] / lseg + s, is <= j (the
@@ -203,16 +210,17 @@ __device__ __forceinline__ int segment_owner(const ScanParams &a, int j, int lan
 
 // YP: bf16 parts of M and the state in y; OUT: outputs wanted; LOCAL: the
 // first launch, which leaves the end states of segments with a successor.
-template <typename TY, int YP, bool OUT, bool LOCAL>
-__global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
-    __shared__ __attribute__((aligned(16))) ScanSmem sm;
+template <typename TY, int YP, bool OUT, bool LOCAL, int NH>
+__global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
+    __shared__ ScanSmem<NH> sm;
+    constexpr int kWaves = 2 * NH, kThreads = 64 * kWaves;
     const ReplayParams &r = a.r;
     const int lane = threadIdx.x & 63, c = lane & 31, hf = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int hpg = r.H / r.G;
 
     if (!LOCAL && blockIdx.x == 0)   // offsets that do not ascend (the mapping below stays within the tensors)
-        for (int i = threadIdx.x; i <= r.batch; i += 256)
+        for (int i = threadIdx.x; i <= r.batch; i += kThreads)
             if (r.cu[i] < 0 || r.cu[i] > r.total || (i && r.cu[i] < r.cu[i - 1])) atomicOr(r.err, kErrSeq);
 
     // Workgroups of one (segment, group) read the same B and C: they follow
@@ -236,15 +244,16 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
     if (b < 0) return;   // padding row
 
     const int hh = wave >> 1;                  // the wave's head among the workgroup's
-    const int hl = hblk * kScanHeads + hh;     // ... within the group
-    const bool live = hl < hpg;                // an odd head count: half a workgroup runs the last head again, unseen
+    const int hl = hblk * NH + hh;             // ... within the group
+    const bool live = hl < hpg;                // waves past the group's heads run its last head again, unseen
     const int h = g * hpg + (live ? hl : hpg - 1);
     const int p0 = (wave & 1) * 32;            // the wave's state rows
+    const int prow = p0 + (c & 16) + 4 * swapped((c >> 2) & 3) + (c & 3);   // ... and the lane's
     const size_t HP = (size_t)r.H * kP, GN = (size_t)r.G * kN;
 
-    // ---- state before the segment: st[nt][i] = S[p0 + c][32 nt + 8 (i / 4) + 4 hf + i % 4]
+    // ---- state before the segment: value i of tile nt is S[prow][32 nt + 16 (i / 8) + 8 hf + i mod 8]
     f16v st0 = (f16v)0.f, st1 = (f16v)0.f, st2 = (f16v)0.f, st3 = (f16v)0.f;
-    const size_t cell = (size_t)(p0 + c) * kN + 4 * hf;
+    const size_t cell = (size_t)prow * kN + 8 * hf;
     auto add_state = [&](const float *s, float f) {
         add_tile(st0, s + cell, f);
         add_tile(st1, s + cell + 32, f);
@@ -278,124 +287,82 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
         }
     }
 
-    const uint16_t *xin = reinterpret_cast<const uint16_t *>(r.x) + (size_t)tok0 * HP;
+    const uint16_t *xin = reinterpret_cast<const uint16_t *>(r.x) + (size_t)tok0 * HP + (size_t)h * kP;
     const uint16_t *Bin = reinterpret_cast<const uint16_t *>(r.Bm) + (size_t)tok0 * GN + (size_t)g * kN;
     const uint16_t *Cin = reinterpret_cast<const uint16_t *>(r.Cm) + (size_t)tok0 * GN + (size_t)g * kN;
     const uint16_t *dtin = reinterpret_cast<const uint16_t *>(r.dt) + (size_t)tok0 * r.H + h;
     TY *yout = reinterpret_cast<TY *>(r.y) + (size_t)tok0 * HP + (size_t)h * kP + p0;
-    const int yoff = (c * (int)HP + 4 * hf) * (int)sizeof(TY);
-    const double A2 = (double)r.A[h] * 1.4426950408889634;
-    const float Dh = r.D[h];
+    const auto scalar = [](float v) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v))); };
+    const float Ah = scalar(r.A[h]), Dh = scalar(r.D[h]);
 
-    // ---- staging roles: 16 quads of tokens x 16 octets of n (B, C); 2 heads x 16 quads x 8 octets of p (x)
-    const int bo = threadIdx.x & 15, bq = threadIdx.x >> 4;
-    const int xo = threadIdx.x & 7, xq = (threadIdx.x >> 3) & 15, xh = threadIdx.x >> 7;
-    const int xhl = hblk * kScanHeads + xh;
-    const size_t xcol = (size_t)(g * hpg + (xhl < hpg ? xhl : hpg - 1)) * kP + 8 * xo;
-    u4v rB[4], rC[4], rX[4];
-    float rdt;
-    // Buffer loads: the chunk's first row is the (uniform) base, and rows past
-    // the segment fall outside the resource and read as zeros.
+    // ---- staging: a wave's load covers 4 rows of B or C (lane: row lane / 16,
+    // piece lane mod 16) or 8 rows of x (row lane / 8, piece lane mod 8).  The
+    // chunk's first row is the (uniform) base; rows past the segment fall
+    // outside the buffer resource and arrive as zeros.
     const int bpitch = (int)GN * 2, xpitch = (int)HP * 2;
-    const int boff = 16 * bo + 4 * bq * bpitch, xoff = (int)xcol * 2 + 4 * xq * xpitch, doff = 2 * lane * r.H;
-    auto fetch = [&](int t0) {
+    float dt_next;
+    auto fetch = [&](int t0, int buf) {
+        typedef __attribute__((address_space(3))) void lds_void;
         const int left = len - t0 < 0 ? 0 : (len - t0 < kQ ? len - t0 : kQ);
         const int rem = __builtin_amdgcn_readfirstlane(left);   // (a vector clamp would make the resources vector values)
-        const int bv = recomputed(boff), xv = recomputed(xoff);
         const auto bs = uniform_rsrc(Bin + (size_t)t0 * GN, rem * bpitch);
+        const auto cs = uniform_rsrc(Cin + (size_t)t0 * GN, OUT ? rem * bpitch : 0);
         const auto xs = uniform_rsrc(xin + (size_t)t0 * HP, rem * xpitch);
         const auto ds = uniform_rsrc(dtin + (size_t)t0 * r.H, rem * 2 * r.H);
+        auto &ch = sm.chunk[buf];
+        const int l = lane_again(), bl = l >> 4, xl = l >> 3;
+        const int boff = bl * bpitch + 16 * ((l & 15) ^ (2 * bl));
+        const int xoff = xl * xpitch + 16 * ((l & 7) ^ (2 * ((xl >> 1) & 3)));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            rB[i] = __builtin_amdgcn_raw_buffer_load_b128(bs, bv + i * bpitch, 0, 0);
-            rX[i] = __builtin_amdgcn_raw_buffer_load_b128(xs, xv + i * xpitch, 0, 0);
+        for (int n = 0; n < 16 / kWaves; ++n) {   // rows 4 i + bl: an odd i turns the pairs by 4 more
+            const int i = wave * (16 / kWaves) + n;
+            const int off = (boff ^ (128 * (i & 1))) + 4 * i * bpitch;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(bs, (lds_void *)ch.B[4 * i], 16, off, 0, 0, 0);
+            if (OUT) __builtin_amdgcn_raw_ptr_buffer_load_lds(cs, (lds_void *)ch.C[4 * i], 16, off, 0, 0, 0);
         }
-        if (OUT) {
-            const auto cs = uniform_rsrc(Cin + (size_t)t0 * GN, rem * bpitch);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) rC[i] = __builtin_amdgcn_raw_buffer_load_b128(cs, bv + i * bpitch, 0, 0);
+        for (int n = 0; n < 4; ++n) {   // a head's two waves take half of its rows each
+            const int i = (wave & 1) * 4 + n;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xs, (lds_void *)ch.x[hh][8 * i], 16, xoff + 8 * i * xpitch, 0, 0, 0);
         }
-        rdt = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ds, doff, 0, 0) << 16);
+        dt_next = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ds, 2 * l * r.H, 0, 0) << 16);
     };
-
-    // LDS offsets of the staging and of the operands
-    const int at_b = quad_at(bq), at_x = quad_at(xq);
-    const int put_b0 = piece_offset(8 * bo, at_b >> 1) + 8 * (at_b & 1);
-    const int put_x0 = (int)sizeof(sm.XT[0]) * xh + piece_offset(8 * xo, at_x >> 1) + 8 * (at_x & 1);
-    const int put_r = 2 * kRowN * 4 * bq + 8 * quad_at(2 * bo);
-    const int get_x0 = (int)sizeof(sm.XT[0]) * hh + piece_offset(p0 + c, hf);
-    const int get_b0 = piece_offset(c, hf);
-    const int get_r = 2 * kRowN * c + 16 * hf;
-
     double total = 0.0;   // decay of the segment (LOCAL)
-    fetch(0);
-    int odd = 0;
-    if (threadIdx.x < 2) sm.bad[threadIdx.x] = kQ;
-    for (int t0 = 0; t0 < len; odd ^= 1) {
-        __syncthreads();   // the previous chunk's LDS reads are done
-        {
-            const int put_b = recomputed(put_b0), put_x = recomputed(put_x0);
-            store_columns(reinterpret_cast<char *>(sm.BT), put_b, rB[0], rB[1], rB[2], rB[3]);
-            if (OUT) {   // quads 2 bo and 2 bo + 1 of a row are two positions apart
-                char *pb = reinterpret_cast<char *>(sm.B) + put_r, *pc = reinterpret_cast<char *>(sm.C) + put_r;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    *reinterpret_cast<u2v *>(pb + 2 * kRowN * i) = u2v{rB[i].x, rB[i].y};
-                    *reinterpret_cast<u2v *>(pb + 2 * kRowN * i + 16) = u2v{rB[i].z, rB[i].w};
-                    *reinterpret_cast<u2v *>(pc + 2 * kRowN * i) = u2v{rC[i].x, rC[i].y};
-                    *reinterpret_cast<u2v *>(pc + 2 * kRowN * i + 16) = u2v{rC[i].z, rC[i].w};
-                }
-            }
-            store_columns(reinterpret_cast<char *>(sm.XT), put_x, rX[0], rX[1], rX[2], rX[3]);
-        }
-        int q = len - t0 < kQ ? len - t0 : kQ;   // tokens of this chunk
-        if (OUT) {
-            // M_tj = 0 for j > t does not keep a non-finite x_j out of y_t: a
-            // chunk ends before a token that holds one, which is then taken alone.
-            unsigned seen = 0;
-            int first = kQ;
-#pragma unroll
-            for (int i = 3; i >= 0; --i) {
-                unsigned bits = 0;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) bits |= (rX[i][d] & 0x7F807F80u) + 0x00800080u;
-                if (bits & 0x80008000u) first = 4 * xq + i;
-                seen |= bits;
-            }
-            if (seen & 0x80008000u) atomicMin(&sm.bad[odd], first);
-        }
+    fetch(0, 0);
+    int buf = 0;
+    for (int t0 = 0; t0 < len; t0 += kQ, buf ^= 1) {
+        const int q = len - t0 < kQ ? len - t0 : kQ;   // tokens of this chunk
+        // The chunk has arrived (every wave waits for its own loads) and the
+        // other buffer's reads are done: the next chunk goes there.
+        // Only the last chunk's stores, issued after its loads, may be outstanding.
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(OUT ? (int)sizeof(TY) * 2 : 0) : "memory");
+        const float dt = dt_next;
         __syncthreads();
-        if (OUT) {
-            const int bad = __builtin_amdgcn_readfirstlane(sm.bad[odd]), stop = bad > 0 ? bad : 1;
-            if (threadIdx.x == 0) sm.bad[odd ^ 1] = kQ;   // read in the last chunk, set in the next
-            if (stop < q) {
-                q = stop;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (4 * xq + i >= q) rX[i] = (u4v)0u;
-                store_columns(reinterpret_cast<char *>(sm.XT), recomputed(put_x0), rX[0], rX[1], rX[2], rX[3]);
-                if (lane >= q) rdt = 0.f;
-                __syncthreads();
-            }
-        }
-
-        const int t1 = t0 + q;
-        const char *xt = reinterpret_cast<const char *>(sm.XT), *bt = reinterpret_cast<const char *>(sm.BT);
-        const int get_x = recomputed(get_x0), get_b = recomputed(get_b0);
+        fetch(t0 + kQ, buf ^ 1);
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- operand addresses within the chunk's buffer
+        const int ln = lane_again(), col = ln & 31, half = ln >> 5, row4 = 4 * half;
+        const int get_r = 256 * col + 16 * half + 32 * (col & 7);   // row col of B, C: ^ 32 ks
+        // transposing reads: row tr of a quarter wave's four, column quad tc, 16-column half tg
+        const int tr = (ln >> 2) & 3, tc = 8 * swapped(ln & 3), tg = (ln >> 4) & 1, tj = row4 + tr;
+        const int get_b = 256 * tj + 32 * (tg ^ tj) + tc;                                       // ^ 64 nt, + 4096 js
+        const int get_x = 128 * tj + 32 * ((2 * (wave & 1) + tg) ^ ((tj >> 1) & 3)) + tc;       // + 2048 js
+        const int get_y = 128 * col + 32 * ((2 * (wave & 1)) ^ ((col >> 1) & 3)) + 16 * half;   // row col of x: ^ 32 s
+        const int yoff = (col * (int)HP + 8 * half) * (int)sizeof(TY);
+        const char *ldsB = sm.chunk[buf].B[0], *ldsC = sm.chunk[buf].C[0], *ldsX = sm.chunk[buf].x[hh][0];
 
         // ---- decays of the wave's head (both waves of a head compute them).
         // exp(c_t - c_j) = 2^(k_t - k_j) 2^f_t 2^-f_j: the fractions' powers
         // are taken once per token, the whole part moves an exponent exactly.
         float lam;
         auto decays = [&]() {
-            const double cum = prefix(A2 * (double)rdt), whole = __builtin_floor(cum);
+            const double cum = prefix((double)Ah * 1.4426950408889634 * (double)dt), whole = __builtin_floor(cum);
             const double c63 = lane_d(cum, 63);
-            const float f = (float)(cum - whole), ri = __builtin_amdgcn_exp2f(-f);
-            sm.k[wave][lane] = (int)whole;
-            sm.cf[wave][lane] = rdt * ri;
-            sm.w[wave][lane] = rdt * __builtin_amdgcn_exp2f((float)(c63 - cum));
-            sm.rf[wave][lane] = __builtin_amdgcn_exp2f(f);
-            sm.ri[wave][lane] = ri;
+            const float f = (float)(cum - whole);
+            sm.k[wave][ln] = (int)whole;
+            sm.cf[wave][ln] = dt * __builtin_amdgcn_exp2f(-f);
+            sm.w[wave][ln] = dt * __builtin_amdgcn_exp2f((float)(c63 - cum));
+            sm.rf[wave][ln] = __builtin_amdgcn_exp2f(f);
             lam = __builtin_amdgcn_exp2f((float)c63);
             total += c63;
             __builtin_amdgcn_wave_barrier();
@@ -408,9 +375,9 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
             auto step = [&](const f16v &tile, int ks) {
                 b8v s[YP];
                 split<YP>(half_of(tile, ks & 1), s);
-                const char *pb = reinterpret_cast<const char *>(sm.B) + get_r + 32 * ks;
-                const char *pc = reinterpret_cast<const char *>(sm.C) + get_r + 32 * ks;
-                const b8v b0 = operand(pb), b1 = operand(pb + 64 * kRowN), c0 = operand(pc), c1 = operand(pc + 64 * kRowN);
+                const int off = get_r ^ (32 * ks);
+                const b8v b0 = operand(ldsB + off), b1 = operand(ldsB + off + 32 * 256);
+                const b8v c0 = operand(ldsC + off), c1 = operand(ldsC + off + 32 * 256);
                 g00 = mfma(b0, c0, g00);
                 g01 = mfma(b0, c1, g01);
                 g11 = mfma(b1, c1, g11);
@@ -422,72 +389,113 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
             };
             step(st0, 0);
             step(st0, 1);
+            __builtin_amdgcn_sched_barrier(0);
             step(st1, 2);
             step(st1, 3);
+            __builtin_amdgcn_sched_barrier(0);
             step(st2, 4);
             step(st2, 5);
+            __builtin_amdgcn_sched_barrier(0);
             step(st3, 6);
             step(st3, 7);
             decays();
-            const int k0 = sm.k[wave][c], k1 = sm.k[wave][32 + c];
-            const float r0 = sm.rf[wave][c], r1 = sm.rf[wave][32 + c];
-            const float D0 = Dh * sm.ri[wave][c], D1 = Dh * sm.ri[wave][32 + c];
+            // the Gram products stay here: moved down to their uses they would keep all their operands in registers
+            asm volatile("" : "+v"(g00), "+v"(g01), "+v"(g11));
+            const int k0 = sm.k[wave][col], k1 = sm.k[wave][32 + col];
+            const float r0 = sm.rf[wave][col], r1 = sm.rf[wave][32 + col];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 y0[i] = __builtin_ldexpf(y0[i], k0);
                 y1[i] = __builtin_ldexpf(y1[i], k1);
             }
-            // ---- y^T += x^T M^T without the factor 2^f_t, M^T as the operand straight from the Gram accumulators
-            auto apply = [&](const f16v &gram, int jt, int kt, float Dt, bool diag, f16v &y) {
+            // M_tj = 0 for j > t does not keep a non-finite x_j out of y_t: in a
+            // chunk that holds one, such values are taken out of the operand, and
+            // the outputs of their row are marked from their token on.
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd |= non_finite(operand(ldsX + (get_y ^ (32 * (i & 1))) + 32 * 128 * (i >> 1)));
+            const int upto = col - row4;
+            auto tail = [&](auto is_odd) {
+                constexpr bool kOdd = decltype(is_odd)::value;
+                if constexpr (kOdd) {
+                    asm volatile("" : "+v"(g00), "+v"(g01), "+v"(g11));   // nothing shared with the other instance
+                    auto mark = [&](f16v &y, int from) {   // from: token of the lane less row4
+                        f16v bad = (f16v)0.f;
+                        for (int js = 0; js < 4; ++js) {
+                            const u4v v = __builtin_bit_cast(u4v, operand_t<128>(ldsX + get_x + 2048 * js));
+                            u4v is, up;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {   // 0x3F80 is 1 in bf16
+                                is[i] = ((v[i] & 0x7F80u) == 0x7F80u) * 0x3F80u | ((v[i] & 0x7F800000u) == 0x7F800000u) * 0x3F800000u;
+                                const int j = 16 * js + 8 * (i >> 1) + 2 * (i & 1);
+                                up[i] = (j <= from) * 0x3F80u | (j < from) * 0x3F800000u;
+                            }
+                            bad = mfma(__builtin_bit_cast(b8v, is), __builtin_bit_cast(b8v, up), bad);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)   // (added to, a NaN stays one)
+                            if (bad[i] != 0.f) y[i] = __builtin_nanf("");
+                        __builtin_amdgcn_sched_barrier(0);
+                    };
+                    mark(y0, upto);
+                    mark(y1, upto + 32);
+                }
+            // ---- y^T += x^T M^T without D and the factor 2^f_t, M^T as the operand straight from the Gram accumulators
+            auto apply = [&](const f16v &gram, int jt, int kt, bool diag, f16v &y) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const int j0 = 32 * jt + 16 * s + 4 * hf;
+                    const int j0 = 32 * jt + 16 * s + row4;
                     f8v m = half_of(gram, s);
                     const f8v cf = read8(&sm.cf[wave][j0]);
                     const i8v kj = read8(&sm.k[wave][j0]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         m[i] = __builtin_ldexpf(m[i] * cf[i], kt - kj[i]);
-                        if (diag) {
-                            const int j = 16 * s + 4 * hf + 8 * (i >> 2) + (i & 3);
-                            m[i] = j < c ? m[i] : (j == c ? m[i] + Dt : 0.f);
-                        }
+                        if (diag) m[i] = 16 * s + 8 * (i >> 2) + (i & 3) <= upto ? m[i] : 0.f;
                     }
                     b8v part[YP];
                     split<YP>(m, part);
-                    const b8v x = operand(xt + (get_x ^ (64 * jt + 32 * s)));
+                    b8v x = operand_t<128>(ldsX + get_x + 4096 * jt + 2048 * s);
+                    if constexpr (kOdd) {
+                        u4v v = __builtin_bit_cast(u4v, x);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] &= ~(((v[i] & 0x7F80u) == 0x7F80u) * 0xFFFFu | ((v[i] & 0x7F800000u) == 0x7F800000u) * 0xFFFF0000u);
+                        x = __builtin_bit_cast(b8v, v);
+                    }
 #pragma unroll
                     for (int i = YP - 1; i >= 0; --i) y = mfma(x, part[i], y);
                 }
             };
-            apply(g00, 0, k0, D0, true, y0);
-            apply(g01, 0, k1, 0.f, false, y1);
-            apply(g11, 1, k1, D1, true, y1);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                y0[i] *= r0;
-                y1[i] *= r1;
-            }
-            // rows past the chunk (and an unseen head's) fall outside the resource
+            apply(g00, 0, k0, true, y0);
+            apply(g01, 0, k1, false, y1);
+            apply(g11, 1, k1, true, y1);
+            // ---- out: y = 2^f_t y + D x; rows past the chunk (and an unseen head's) fall outside the resource
             const auto ys = uniform_rsrc(yout + (size_t)t0 * HP, live ? q * (int)HP * (int)sizeof(TY) : 0);
-            auto store = [&](const f16v &y, int off) {
+            auto store = [&](const f16v &y, float rt, int tt) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f4v v = {y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]};
-                    const int at = off + 8 * i * (int)sizeof(TY);
-                    if constexpr (sizeof(TY) == 4)
-                        __builtin_amdgcn_raw_buffer_store_b128(v, ys, at, 0, 0);
-                    else
-                        __builtin_amdgcn_raw_buffer_store_b64(
-                            __builtin_bit_cast(u2v, __builtin_convertvector(v, b4v)), ys, at, 0, 0);
+                for (int s = 0; s < 2; ++s) {
+                    const f8v x = vec8<uint16_t>::widen(__builtin_bit_cast(u4u, operand(ldsX + (get_y ^ (32 * s)) + 32 * 128 * tt)));
+                    f8v v = half_of(y, s);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = fmaf(Dh, x[i], v[i] * rt);
+                    const int at = yoff + (32 * tt * (int)HP + 16 * s) * (int)sizeof(TY);
+                    if constexpr (sizeof(TY) == 4) {
+                        __builtin_amdgcn_raw_buffer_store_b128(f4v{v[0], v[1], v[2], v[3]}, ys, at, 0, 0);
+                        __builtin_amdgcn_raw_buffer_store_b128(f4v{v[4], v[5], v[6], v[7]}, ys, at + 16, 0, 0);
+                    } else {
+                        b8v o[1];
+                        split<1>(v, o);
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, o[0]), ys, at, 0, 0);
+                    }
                 }
             };
-            store(y0, yoff);
-            store(y1, yoff + 32 * (int)HP * (int)sizeof(TY));
+            store(y0, r0, 0);
+            store(y1, r1, 1);
+            };
+            if (__builtin_amdgcn_ballot_w64(odd) != 0) tail(std::true_type{});
+            else tail(std::false_type{});
         }
-        // The next chunk is requested here, when only the state is held.
-        __builtin_amdgcn_sched_barrier(0);
-        fetch(t1);
 
         // ---- S^T[n][p] = exp(c_63) S^T + sum_j B_j[n] (w_j x_j[p])
 #pragma unroll
@@ -499,15 +507,15 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
         }
 #pragma unroll
         for (int js = 0; js < 4; ++js) {
-            f8v v = vec8<uint16_t>::widen(*reinterpret_cast<const u4v *>(__builtin_assume_aligned(xt + (get_x ^ (32 * js)), 16)));
-            const f8v w = read8(&sm.w[wave][16 * js + 4 * hf]);
+            f8v v = vec8<uint16_t>::widen(__builtin_bit_cast(u4u, operand_t<128>(ldsX + get_x + 2048 * js)));
+            const f8v w = read8(&sm.w[wave][16 * js + row4]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= w[i];
             b8v part[3];
             split<3>(v, part);
-            const b8v b0 = operand(bt + (get_b ^ (32 * js))), b1 = operand(bt + (get_b ^ (32 * (js ^ 1))) + 64 * kRowQ),
-                      b2 = operand(bt + (get_b ^ (32 * (js ^ 2))) + 128 * kRowQ),
-                      b3 = operand(bt + (get_b ^ (32 * (js ^ 3))) + 192 * kRowQ);
+            const char *pb = ldsB + 4096 * js;
+            const b8v b0 = operand_t<256>(pb + get_b), b1 = operand_t<256>(pb + (get_b ^ 64)),
+                      b2 = operand_t<256>(pb + (get_b ^ 128)), b3 = operand_t<256>(pb + (get_b ^ 192));
 #pragma unroll
             for (int i = 2; i >= 0; --i) {
                 st0 = mfma(b0, part[i], st0);
@@ -516,7 +524,6 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
                 st3 = mfma(b3, part[i], st3);
             }
         }
-        t0 = t1;
     }
 
     if (LOCAL) {
@@ -529,6 +536,15 @@ __global__ void __launch_bounds__(256, 2) scan_kernel(ScanParams a) {
         if (live) put_state(ckpt);
         publish_position(r, b, 0, true, -1);
     }
+}
+
+template <int NH>
+void launch_heads(const ScanParams &a, bool outputs, dim3 grid, hipStream_t s) {
+    const dim3 block(128 * NH);
+    if (a.nfull) hipLaunchKernelGGL((scan_kernel<float, 3, false, true, NH>), grid, block, 0, s, a);
+    if (!outputs) hipLaunchKernelGGL((scan_kernel<float, 3, false, false, NH>), grid, block, 0, s, a);
+    else if (a.r.y_bf16) hipLaunchKernelGGL((scan_kernel<uint16_t, 2, true, false, NH>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((scan_kernel<float, 3, true, false, NH>), grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -548,15 +564,15 @@ hipError_t launch_scan(const ReplayParams &p, bool outputs, void *workspace, hip
         a.lam = a.s0 + (size_t)a.nfull * p.H * kP * kN;
     }
     a.nseg = (int)(p.total / a.lseg) + p.batch;
-    a.hb = (p.H / p.G + kScanHeads - 1) / kScanHeads;
+    const int nh = scan_heads(p.H / p.G);
+    a.hb = (p.H / p.G + nh - 1) / nh;
     a.r.wg_per_slot = p.G * a.hb;
     const int64_t blocks = ((int64_t)a.nseg * p.G + 7) / 8 * 8 * a.hb;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks), block(256);
-    if (a.nfull) hipLaunchKernelGGL((scan_kernel<float, 3, false, true>), grid, block, 0, s, a);
-    if (!outputs) hipLaunchKernelGGL((scan_kernel<float, 3, false, false>), grid, block, 0, s, a);
-    else if (p.y_bf16) hipLaunchKernelGGL((scan_kernel<uint16_t, 2, true, false>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((scan_kernel<float, 3, true, false>), grid, block, 0, s, a);
+    const dim3 grid((unsigned)blocks);
+    if (nh == 4) launch_heads<4>(a, outputs, grid, s);
+    else if (nh == 2) launch_heads<2>(a, outputs, grid, s);
+    else launch_heads<1>(a, outputs, grid, s);
     return hipGetLastError();
 }
 
