@@ -41,8 +41,6 @@
 #include "replay_common.h"
 #include "scan.h"
 
-#include <type_traits>
-
 namespace rssm {
 namespace {
 
@@ -174,13 +172,37 @@ __device__ __forceinline__ double prefix(double v) {
     return v;
 }
 
-// The lane number, opaque to the compiler: what is derived from it inside the
-// chunk loop is derived again in every chunk and held in no register between
-// (the accumulators need them all).
+// The lane number, derived again wherever it is asked for (two instructions):
+// a chunk's addresses come from it and are held in no register between chunks,
+// where a spilled one would wait for the loads in flight.
 __device__ __forceinline__ int lane_again() {
-    int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
-    asm volatile("" : "+v"(l));
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
     return l;
+}
+
+// 16 bytes a lane from byte offset `off` of the buffer resource (zeros outside
+// it) to the wave's 1024 bytes of LDS at `lds`.  Written out rather than by the
+// builtin, which makes the compiler wait for it before the transposing reads
+// of the other buffer; the kernel waits for it itself (vmcnt) at the end of a
+// chunk.  Nothing is loaded to a register; m0, the LDS base, is set and used
+// here (the compiler sets it anew before each use of its own).
+__device__ __forceinline__ void load_to_lds(u4v resource, int off, unsigned lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(resource),
+                 "s"(lds)
+                 : "memory");
+}
+
+__device__ __forceinline__ u4v resource_of(const void *p, int bytes) {   // a wave-uniform address
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    return u4v{(unsigned)__builtin_amdgcn_readfirstlane((unsigned)u),
+               (unsigned)__builtin_amdgcn_readfirstlane((unsigned)(u >> 32)) & 0xFFFFu, (unsigned)bytes,
+               (unsigned)kBufferRsrcWord3};
+}
+
+__device__ __forceinline__ unsigned lds_offset(const void *p) {
+    typedef __attribute__((address_space(3))) const void lds_void;
+    return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(lds_void *)p);
 }
 
 // Exponent all ones in either half of any of the operand's dwords.
@@ -300,15 +322,12 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
     // chunk's first row is the (uniform) base; rows past the segment fall
     // outside the buffer resource and arrive as zeros.
     const int bpitch = (int)GN * 2, xpitch = (int)HP * 2;
-    float dt_next;
     auto fetch = [&](int t0, int buf) {
-        typedef __attribute__((address_space(3))) void lds_void;
         const int left = len - t0 < 0 ? 0 : (len - t0 < kQ ? len - t0 : kQ);
         const int rem = __builtin_amdgcn_readfirstlane(left);   // (a vector clamp would make the resources vector values)
-        const auto bs = uniform_rsrc(Bin + (size_t)t0 * GN, rem * bpitch);
-        const auto cs = uniform_rsrc(Cin + (size_t)t0 * GN, OUT ? rem * bpitch : 0);
-        const auto xs = uniform_rsrc(xin + (size_t)t0 * HP, rem * xpitch);
-        const auto ds = uniform_rsrc(dtin + (size_t)t0 * r.H, rem * 2 * r.H);
+        const u4v bs = resource_of(Bin + (size_t)t0 * GN, rem * bpitch);
+        const u4v cs = resource_of(Cin + (size_t)t0 * GN, OUT ? rem * bpitch : 0);
+        const u4v xs = resource_of(xin + (size_t)t0 * HP, rem * xpitch);
         auto &ch = sm.chunk[buf];
         const int l = lane_again(), bl = l >> 4, xl = l >> 3;
         const int boff = bl * bpitch + 16 * ((l & 15) ^ (2 * bl));
@@ -317,26 +336,31 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
         for (int n = 0; n < 16 / kWaves; ++n) {   // rows 4 i + bl: an odd i turns the pairs by 4 more
             const int i = wave * (16 / kWaves) + n;
             const int off = (boff ^ (128 * (i & 1))) + 4 * i * bpitch;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(bs, (lds_void *)ch.B[4 * i], 16, off, 0, 0, 0);
-            if (OUT) __builtin_amdgcn_raw_ptr_buffer_load_lds(cs, (lds_void *)ch.C[4 * i], 16, off, 0, 0, 0);
+            load_to_lds(bs, off, lds_offset(ch.B[4 * i]));
+            if (OUT) load_to_lds(cs, off, lds_offset(ch.C[4 * i]));
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {   // a head's two waves take half of its rows each
             const int i = (wave & 1) * 4 + n;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xs, (lds_void *)ch.x[hh][8 * i], 16, xoff + 8 * i * xpitch, 0, 0, 0);
+            load_to_lds(xs, xoff + 8 * i * xpitch, lds_offset(ch.x[hh][8 * i]));
         }
-        dt_next = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(ds, 2 * l * r.H, 0, 0) << 16);
+    };
+    // dt of the lane's token in the chunk at t0
+    auto fetch_dt = [&](int t0) {
+        const int left = len - t0 < 0 ? 0 : (len - t0 < kQ ? len - t0 : kQ);
+        const auto ds = uniform_rsrc(dtin + (size_t)t0 * r.H, __builtin_amdgcn_readfirstlane(left) * 2 * r.H);
+        return __builtin_amdgcn_raw_buffer_load_b16(ds, 2 * lane_again() * r.H, 0, 0);
     };
     double total = 0.0;   // decay of the segment (LOCAL)
     fetch(0, 0);
+    unsigned dt_bits = fetch_dt(0);
     int buf = 0;
     for (int t0 = 0; t0 < len; t0 += kQ, buf ^= 1) {
         const int q = len - t0 < kQ ? len - t0 : kQ;   // tokens of this chunk
         // The chunk has arrived (every wave waits for its own loads) and the
         // other buffer's reads are done: the next chunk goes there.
-        // Only the last chunk's stores, issued after its loads, may be outstanding.
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(OUT ? (int)sizeof(TY) * 2 : 0) : "memory");
-        const float dt = dt_next;
+        asm volatile("s_waitcnt vmcnt(0)" : "+v"(dt_bits)::"memory");   // (dt too: not waited for behind the next loads)
+        const float dt = __uint_as_float((uint32_t)dt_bits << 16);
         __syncthreads();
         fetch(t0 + kQ, buf ^ 1);
         __builtin_amdgcn_sched_barrier(0);
@@ -356,7 +380,9 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
         // are taken once per token, the whole part moves an exponent exactly.
         float lam;
         auto decays = [&]() {
-            const double cum = prefix((double)Ah * 1.4426950408889634 * (double)dt), whole = __builtin_floor(cum);
+            float A = Ah;
+            asm volatile("" : "+s"(A));   // (its product is not held in vector registers)
+            const double cum = prefix((double)A * 1.4426950408889634 * (double)dt), whole = __builtin_floor(cum);
             const double c63 = lane_d(cum, 63);
             const float f = (float)(cum - whole);
             sm.k[wave][ln] = (int)whole;
@@ -369,6 +395,7 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
         };
         if (!OUT) decays();
 
+        unsigned bad_row = 0;   // the lane's row has a non-finite x in this chunk
         if (OUT) {
             // ---- y^T[p][t] = sum_n S[p][n] C_t[n] and the Gram tiles G^T[j][t] = B_j . C_t
             f16v y0 = (f16v)0.f, y1 = (f16v)0.f, g00 = (f16v)0.f, g01 = (f16v)0.f, g11 = (f16v)0.f;
@@ -408,38 +435,48 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
                 y0[i] = __builtin_ldexpf(y0[i], k0);
                 y1[i] = __builtin_ldexpf(y1[i], k1);
             }
-            // M_tj = 0 for j > t does not keep a non-finite x_j out of y_t: in a
-            // chunk that holds one, such values are taken out of the operand, and
-            // the outputs of their row are marked from their token on.
+            // M_tj = 0 for j > t does not keep a non-finite x_j out of y_t.  A
+            // wave that meets one marks the outputs of its row from its token on,
+            // notes the row for the state and takes the value out of its half of
+            // x (which no other wave reads).
             bool odd = false;
 #pragma unroll
             for (int i = 0; i < 4; ++i) odd |= non_finite(operand(ldsX + (get_y ^ (32 * (i & 1))) + 32 * 128 * (i >> 1)));
             const int upto = col - row4;
-            auto tail = [&](auto is_odd) {
-                constexpr bool kOdd = decltype(is_odd)::value;
-                if constexpr (kOdd) {
-                    asm volatile("" : "+v"(g00), "+v"(g01), "+v"(g11));   // nothing shared with the other instance
-                    auto mark = [&](f16v &y, int from) {   // from: token of the lane less row4
-                        f16v bad = (f16v)0.f;
-                        for (int js = 0; js < 4; ++js) {
-                            const u4v v = __builtin_bit_cast(u4v, operand_t<128>(ldsX + get_x + 2048 * js));
-                            u4v is, up;
+            if (__builtin_amdgcn_ballot_w64(odd) != 0) {
+                auto mark = [&](f16v &y, int from) {   // from: token of the lane less row4
+                    f16v bad = (f16v)0.f;
+                    for (int js = 0; js < 4; ++js) {
+                        const u4v v = __builtin_bit_cast(u4v, operand_t<128>(ldsX + get_x + 2048 * js));
+                        u4v is, up;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {   // 0x3F80 is 1 in bf16
-                                is[i] = ((v[i] & 0x7F80u) == 0x7F80u) * 0x3F80u | ((v[i] & 0x7F800000u) == 0x7F800000u) * 0x3F800000u;
-                                const int j = 16 * js + 8 * (i >> 1) + 2 * (i & 1);
-                                up[i] = (j <= from) * 0x3F80u | (j < from) * 0x3F800000u;
-                            }
-                            bad = mfma(__builtin_bit_cast(b8v, is), __builtin_bit_cast(b8v, up), bad);
+                        for (int i = 0; i < 4; ++i) {   // 0x3F80 is 1 in bf16
+                            is[i] = ((v[i] & 0x7F80u) == 0x7F80u) * 0x3F80u | ((v[i] & 0x7F800000u) == 0x7F800000u) * 0x3F800000u;
+                            const int j = 16 * js + 8 * (i >> 1) + 2 * (i & 1);
+                            up[i] = (j <= from) * 0x3F80u | (j < from) * 0x3F800000u;
+                            bad_row |= is[i];
                         }
+                        bad = mfma(__builtin_bit_cast(b8v, is), __builtin_bit_cast(b8v, up), bad);
+                    }
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)   // (added to, a NaN stays one)
-                            if (bad[i] != 0.f) y[i] = __builtin_nanf("");
-                        __builtin_amdgcn_sched_barrier(0);
-                    };
-                    mark(y0, upto);
-                    mark(y1, upto + 32);
+                    for (int i = 0; i < 16; ++i)   // (added to, a NaN stays one)
+                        if (bad[i] != 0.f) y[i] = __builtin_nanf("");
+                    __builtin_amdgcn_sched_barrier(0);
+                };
+                mark(y0, upto);
+                mark(y1, upto + 32);
+                bad_row |= __shfl_xor(bad_row, 32);   // a row's tokens are spread over both halves
+                for (int i = 0; i < 4; ++i) {
+                    const char *p = ldsX + (get_y ^ (32 * (i & 1))) + 32 * 128 * (i >> 1);
+                    u4v v = __builtin_bit_cast(u4v, operand(p));
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        v[d] &= ~(((v[d] & 0x7F80u) == 0x7F80u) * 0xFFFFu | ((v[d] & 0x7F800000u) == 0x7F800000u) * 0xFFFF0000u);
+                    // (a store the compiler sees would make it wait for the next chunk's loads)
+                    typedef __attribute__((address_space(3))) const char lds_char;
+                    asm volatile("ds_write_b128 %0, %1" ::"v"((unsigned)(uintptr_t)(lds_char *)p), "v"(v) : "memory");
                 }
+            }
             // ---- y^T += x^T M^T without D and the factor 2^f_t, M^T as the operand straight from the Gram accumulators
             auto apply = [&](const f16v &gram, int jt, int kt, bool diag, f16v &y) {
 #pragma unroll
@@ -455,14 +492,7 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
                     }
                     b8v part[YP];
                     split<YP>(m, part);
-                    b8v x = operand_t<128>(ldsX + get_x + 4096 * jt + 2048 * s);
-                    if constexpr (kOdd) {
-                        u4v v = __builtin_bit_cast(u4v, x);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] &= ~(((v[i] & 0x7F80u) == 0x7F80u) * 0xFFFFu | ((v[i] & 0x7F800000u) == 0x7F800000u) * 0xFFFF0000u);
-                        x = __builtin_bit_cast(b8v, v);
-                    }
+                    const b8v x = operand_t<128>(ldsX + get_x + 4096 * jt + 2048 * s);
 #pragma unroll
                     for (int i = YP - 1; i >= 0; --i) y = mfma(x, part[i], y);
                 }
@@ -492,10 +522,10 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
             };
             store(y0, r0, 0);
             store(y1, r1, 1);
-            };
-            if (__builtin_amdgcn_ballot_w64(odd) != 0) tail(std::true_type{});
-            else tail(std::false_type{});
         }
+
+        // the next chunk's dt, now that the accumulators of y and the Gram tiles are free
+        dt_bits = fetch_dt(t0 + kQ);
 
         // ---- S^T[n][p] = exp(c_63) S^T + sum_j B_j[n] (w_j x_j[p])
 #pragma unroll
@@ -523,6 +553,9 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
                 st2 = mfma(b2, part[i], st2);
                 st3 = mfma(b3, part[i], st3);
             }
+        }
+        if (OUT && __builtin_amdgcn_ballot_w64(bad_row != 0) != 0) {
+            if (bad_row) st0 = st1 = st2 = st3 = (f16v)__builtin_nanf("");
         }
     }
 
