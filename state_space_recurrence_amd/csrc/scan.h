@@ -26,7 +26,10 @@ struct ScanParams {
 };
 
 // Tokens per segment for a call: long sequences are cut so that each of the
-// 256 compute units has a workgroup, and no finer.
+// 256 compute units has a workgroup, and no finer.  (23 sequences of 9001
+// tokens together, 128 heads: 350 us so; cut twice or three times as fine the
+// pieces even out, the second launch takes 305 -> 290 us, but the first one
+// grows from 45 to 95 us.)
 inline int scan_segment(int64_t total, int H, int G) {
     const int nh = scan_heads(H / G);
     const int64_t hb = (int64_t)G * ((H / G + nh - 1) / nh);
@@ -39,8 +42,7 @@ inline int scan_segment(int64_t total, int H, int G) {
 
 inline size_t scan_workspace(int64_t total, int H, int G) {
     const int64_t nfull = total / scan_segment(total, H, G);
-    // a single segment never has a successor
-    return nfull == 0 ? 0 : (size_t)nfull * H * (2 * 64 * 128 + 1) * sizeof(float);
+    return (size_t)nfull * H * (2 * 64 * 128 + 1) * sizeof(float);
 }
 
 // bf16 inputs, fp32 checkpoints.  p.loc etc. may be NULL when workspace is

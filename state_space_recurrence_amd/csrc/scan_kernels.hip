@@ -35,7 +35,9 @@
 // cut into segments: a first launch leaves each segment's end state (the first
 // from the slot's state, the others from zero), and in the second every
 // segment joins the states before it, S = loc_{k-1} + lam_{k-1} (loc_{k-2} +
-// ...), before it runs its tokens.
+// ...), before it runs its tokens.  Both sums end where the decay is exactly
+// zero in fp32: what lies before cannot change them (nor can a non-finite
+// value there, which a token by token recurrence would carry on).
 #include "device_common.h"
 #include "mixer_device.h"
 #include "replay_common.h"
@@ -67,6 +69,7 @@ struct ScanSmem {
     alignas(16) float cf[2 * NH][kQ];         // dt_j 2^-f_j
     alignas(16) float w[2 * NH][kQ];          // dt_j exp(c_63 - c_j)
     float rf[2 * NH][kQ];                     // 2^f_t
+    int done[2][2 * NH];                      // per wave: nothing before the chunk counts (LOCAL)
 };
 
 // Of each four quads the middle two trade places: row r of a 16-row tile
@@ -144,6 +147,14 @@ __device__ __forceinline__ void put_tile(const f16v &v, float *s) {
     for (int i = 0; i < 4; ++i)
         *reinterpret_cast<float4 *>(s + 4 * i + 8 * (i >> 1)) =
             make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+__device__ __forceinline__ void copy_tile(const float *s, float *d, bool write) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 u = *reinterpret_cast<const float4 *>(s + 4 * i + 8 * (i >> 1));
+        if (write) *reinterpret_cast<float4 *>(d + 4 * i + 8 * (i >> 1)) = u;
+    }
 }
 
 template <int CTRL, int ROWS>
@@ -291,15 +302,14 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
     const size_t headN = (size_t)kP * kN;
     float *ckpt = r.ckpt + ((size_t)b * r.H + h) * headN;
     const size_t ent0 = (size_t)(start / a.lseg);   // the sequence's first full segment in the workspace
-    if (k == 0) {
-        const bool fresh = r.fresh ? r.fresh[seq] != 0 : r.from_zero != 0;
-        if (!fresh) {
-            add_state(LOCAL || last ? ckpt : a.s0 + (ent0 * r.H + h) * headN, 1.f);
-            if ((LOCAL || last) && threadIdx.x == 0 && r.pos[b] != 0) atomicOr(r.err, kErrPos);   // buffer not empty
-            // the second launch rewrites the checkpoint, so its first segment reads a copy
-            if (LOCAL && live) put_state(a.s0 + (ent0 * r.H + h) * headN);
-        }
-    } else if (!LOCAL) {
+    const bool fresh = r.fresh ? r.fresh[seq] != 0 : r.from_zero != 0;
+    float *start_copy = a.s0 + (ent0 * r.H + h) * headN;
+    if (k == 0 && !fresh && (LOCAL || last) && threadIdx.x == 0 && r.pos[b] != 0) atomicOr(r.err, kErrPos);   // buffer not empty
+    if (LOCAL) {
+        // joined at the end
+    } else if (k == 0) {
+        if (!fresh) add_state(last ? ckpt : start_copy, 1.f);
+    } else {
         // a factor of exactly zero ends the sum: nothing before it counts
         float f = 1.f;
         for (int i = k - 1; i >= 0 && f != 0.f; --i) {
@@ -323,7 +333,7 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
     // outside the buffer resource and arrive as zeros.
     const int bpitch = (int)GN * 2, xpitch = (int)HP * 2;
     auto fetch = [&](int t0, int buf) {
-        const int left = len - t0 < 0 ? 0 : (len - t0 < kQ ? len - t0 : kQ);
+        const int left = t0 < 0 || t0 > len ? 0 : (len - t0 < kQ ? len - t0 : kQ);
         const int rem = __builtin_amdgcn_readfirstlane(left);   // (a vector clamp would make the resources vector values)
         const u4v bs = resource_of(Bin + (size_t)t0 * GN, rem * bpitch);
         const u4v cs = resource_of(Cin + (size_t)t0 * GN, OUT ? rem * bpitch : 0);
@@ -347,23 +357,45 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
     };
     // dt of the lane's token in the chunk at t0
     auto fetch_dt = [&](int t0) {
-        const int left = len - t0 < 0 ? 0 : (len - t0 < kQ ? len - t0 : kQ);
+        const int left = t0 < 0 || t0 > len ? 0 : (len - t0 < kQ ? len - t0 : kQ);
         const auto ds = uniform_rsrc(dtin + (size_t)t0 * r.H, __builtin_amdgcn_readfirstlane(left) * 2 * r.H);
         return __builtin_amdgcn_raw_buffer_load_b16(ds, 2 * lane_again() * r.H, 0, 0);
     };
-    double total = 0.0;   // decay of the segment (LOCAL)
-    fetch(0, 0);
-    unsigned dt_bits = fetch_dt(0);
+    // The first launch takes the chunks from the last to the first, each with
+    // its decay to the segment's end (`total`): the accumulators are never
+    // rescaled, and once a head's decay is exactly zero in fp32 its earlier
+    // tokens are not taken at all.
+    constexpr int kStep = LOCAL ? -kQ : kQ;
+    const int t_first = LOCAL ? (len - 1) / kQ * kQ : 0;
+    double total = 0.0;
+    fetch(t_first, 0);
+    unsigned dt_bits = fetch_dt(t_first);
     int buf = 0;
-    for (int t0 = 0; t0 < len; t0 += kQ, buf ^= 1) {
+    for (int t0 = t_first; LOCAL ? t0 >= 0 : t0 < len; t0 += kStep, buf ^= 1) {
         const int q = len - t0 < kQ ? len - t0 : kQ;   // tokens of this chunk
         // The chunk has arrived (every wave waits for its own loads) and the
         // other buffer's reads are done: the next chunk goes there.
+        const bool done = LOCAL && __builtin_amdgcn_exp2f((float)total) == 0.f;
+        if (LOCAL && lane == 0) sm.done[buf][wave] = done;
         asm volatile("s_waitcnt vmcnt(0)" : "+v"(dt_bits)::"memory");   // (dt too: not waited for behind the next loads)
         const float dt = __uint_as_float((uint32_t)dt_bits << 16);
         __syncthreads();
-        fetch(t0 + kQ, buf ^ 1);
+        if (LOCAL) {
+            int all = 1;
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) all &= sm.done[buf][i];
+            if (__builtin_amdgcn_readfirstlane(all)) break;
+        }
+        fetch(t0 + kStep, buf ^ 1);
+        if (LOCAL && done) {
+            dt_bits = 0;
+            continue;
+        }
         __builtin_amdgcn_sched_barrier(0);
+        // A wave's priority falls as it moves through its chunk, so that of the
+        // two on a SIMD the one behind, with products to issue, goes first and
+        // the other's vector work fills in.
+        __builtin_amdgcn_s_setprio(3);
         // ---- operand addresses within the chunk's buffer
         const int ln = lane_again(), col = ln & 31, half = ln >> 5, row4 = 4 * half;
         const int get_r = 256 * col + 16 * half + 32 * (col & 7);   // row col of B, C: ^ 32 ks
@@ -385,12 +417,14 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
             const double cum = prefix((double)A * 1.4426950408889634 * (double)dt), whole = __builtin_floor(cum);
             const double c63 = lane_d(cum, 63);
             const float f = (float)(cum - whole);
-            sm.k[wave][ln] = (int)whole;
-            sm.cf[wave][ln] = dt * __builtin_amdgcn_exp2f(-f);
-            sm.w[wave][ln] = dt * __builtin_amdgcn_exp2f((float)(c63 - cum));
-            sm.rf[wave][ln] = __builtin_amdgcn_exp2f(f);
+            if (OUT) {
+                sm.k[wave][ln] = (int)whole;
+                sm.cf[wave][ln] = dt * __builtin_amdgcn_exp2f(-f);
+                sm.rf[wave][ln] = __builtin_amdgcn_exp2f(f);
+            }
+            sm.w[wave][ln] = dt * __builtin_amdgcn_exp2f((float)(total + c63 - cum));   // (total: 0 but in LOCAL)
             lam = __builtin_amdgcn_exp2f((float)c63);
-            total += c63;
+            if (LOCAL) total += c63;
             __builtin_amdgcn_wave_barrier();
         };
         if (!OUT) decays();
@@ -428,6 +462,7 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
             decays();
             // the Gram products stay here: moved down to their uses they would keep all their operands in registers
             asm volatile("" : "+v"(g00), "+v"(g01), "+v"(g11));
+            __builtin_amdgcn_s_setprio(2);
             const int k0 = sm.k[wave][col], k1 = sm.k[wave][32 + col];
             const float r0 = sm.rf[wave][col], r1 = sm.rf[wave][32 + col];
 #pragma unroll
@@ -500,6 +535,7 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
             apply(g00, 0, k0, true, y0);
             apply(g01, 0, k1, false, y1);
             apply(g11, 1, k1, true, y1);
+            __builtin_amdgcn_s_setprio(1);
             // ---- out: y = 2^f_t y + D x; rows past the chunk (and an unseen head's) fall outside the resource
             const auto ys = uniform_rsrc(yout + (size_t)t0 * HP, live ? q * (int)HP * (int)sizeof(TY) : 0);
             auto store = [&](const f16v &y, float rt, int tt) {
@@ -524,10 +560,12 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
             store(y1, r1, 1);
         }
 
+        __builtin_amdgcn_s_setprio(0);
         // the next chunk's dt, now that the accumulators of y and the Gram tiles are free
         dt_bits = fetch_dt(t0 + kQ);
 
         // ---- S^T[n][p] = exp(c_63) S^T + sum_j B_j[n] (w_j x_j[p])
+        if (!LOCAL)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             st0[i] *= lam;
@@ -559,11 +597,21 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
         }
     }
 
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // loads to LDS still in flight
     if (LOCAL) {
         const size_t e = (ent0 + k) * r.H + h;
+        const float lam = __builtin_amdgcn_exp2f((float)total);
+        if (k == 0 && !fresh) {
+            // the second launch rewrites the checkpoint, so its first segment reads a copy
+            copy_tile(ckpt + cell, start_copy + cell, live);
+            copy_tile(ckpt + cell + 32, start_copy + cell + 32, live);
+            copy_tile(ckpt + cell + 64, start_copy + cell + 64, live);
+            copy_tile(ckpt + cell + 96, start_copy + cell + 96, live);
+            if (lam != 0.f) add_state(ckpt, lam);
+        }
         if (live) {
             put_state(a.loc + e * headN);
-            if ((wave & 1) == 0 && lane == 0) a.lam[e] = exp2f((float)total);
+            if ((wave & 1) == 0 && lane == 0) a.lam[e] = lam;
         }
     } else if (last) {
         if (live) put_state(ckpt);
