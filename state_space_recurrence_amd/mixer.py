@@ -68,8 +68,18 @@ def _lib():
     return L
 
 
-def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """The stream of a call: the given one, or the current one of t's device.
+    (A decode token's calls are bound by the host, so the paths that every
+    call takes are kept short: about 4 us a call.)"""
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw is not None:
+        return _current_raw(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -81,19 +91,25 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _pitch(t: torch.Tensor, lead, width: int, dtype, name: str) -> int:
+def _dense(t: torch.Tensor, shape: tuple, dtype, name: str) -> int:
+    """Address of a dense device tensor of this shape and type (else raise)."""
+    if t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, shape, dtype, name)
+    return t.data_ptr()
+
+
+def _pitch(t: torch.Tensor, lead: tuple, width: int, dtype, name: str) -> int:
     """Elements between consecutive tokens of a view [*lead, width] of a
     projection's rows: innermost dense, tokens evenly spaced."""
-    if tuple(t.shape) != (*lead, width) or t.dtype != dtype or not t.is_cuda:
+    st = t.stride()
+    if t.shape != (*lead, width) or t.dtype is not dtype or not t.is_cuda:
         raise ReplaySSMError(f"{name}: expected device tensor {(*lead, width)} {dtype}, got {tuple(t.shape)} "
                              f"{t.dtype} device={t.device}")
-    st = t.stride()
-    # the token axes that have a stride at all: the last one's is the pitch
-    pitch = width
     if len(lead) == 1:
         pitch = st[0] if lead[0] > 1 else max(st[0], width)
         even = True
-    else:
+    else:   # the last token axis that has a stride at all gives the pitch
         n, T = lead
         pitch = st[1] if T > 1 else (st[0] if n > 1 else max(st[1], width))
         even = n <= 1 or st[0] == T * pitch
@@ -152,35 +168,35 @@ class ConvState:
 
     def _call(self, rows, slots):
         if slots is not None:
-            _need(slots, (rows,), torch.int32, "slots")
-        elif rows != self.batch:
-            raise ReplaySSMError(f"a call without slots covers all {self.batch} slots, got {rows} rows")
+            at = _dense(slots, (rows,), torch.int32, "slots")
+        else:
+            at = None
+            if rows != self.batch:
+                raise ReplaySSMError(f"a call without slots covers all {self.batch} slots, got {rows} rows")
         d = self._desc
         if rows != d.batch:
             d = RssmConvDesc.from_buffer_copy(d)
             d.batch = rows
-        st = RssmConvState(self.ring.data_ptr(), self.head.data_ptr(), self.work.data_ptr(), self.weight.data_ptr(),
-                           _ptr(self.bias), _ptr(self.dt_bias), _ptr(slots))
-        return d, st
+        return d, RssmConvState(self.ring.data_ptr(), self.head.data_ptr(), self.work.data_ptr(),
+                                self.weight.data_ptr(), _ptr(self.bias), _ptr(self.dt_bias), at)
 
     def _io(self, u, dt, lead, out, stream):
-        up = _pitch(u, lead, self.channels, self.in_dtype, "u")
-        dp = _pitch(dt, lead, self.heads, self.in_dtype, "dt")
-        shapes = ((*lead, self.heads, self.head_dim), (*lead, self.groups, self.d_state),
-                  (*lead, self.groups, self.d_state), (*lead, self.heads))
+        ty = self.in_dtype
+        up, dp = _pitch(u, lead, self.channels, ty, "u"), _pitch(dt, lead, self.heads, ty, "dt")
+        head, group = (*lead, self.heads, self.head_dim), (*lead, self.groups, self.d_state)
         if out is None:
-            out = tuple(_empty(s, self.in_dtype, u.device, stream) for s in shapes)
-        else:
-            for t, s, n in zip(out, shapes, ("out x", "out B", "out C", "out dt")):
-                _need(t, s, self.in_dtype, n)
-        return out, RssmConvIO(u.data_ptr(), up, dt.data_ptr(), dp, *(t.data_ptr() for t in out))
+            out = tuple(_empty(s, ty, u.device, stream) for s in (head, group, group, (*lead, self.heads)))
+        x, B, C, d = out
+        return out, RssmConvIO(u.data_ptr(), up, dt.data_ptr(), dp, _dense(x, head, ty, "out x"),
+                               _dense(B, group, ty, "out B"), _dense(C, group, ty, "out C"),
+                               _dense(d, (*lead, self.heads), ty, "out dt"))
 
     def check_device_errors(self, stream=None) -> None:
         """Raise if a call on this state met a device-side range error (synchronises)."""
         from . import RssmState
         st = RssmState()
         st.work = self.work.data_ptr()
-        _check(lib().replayssm_check_device_errors(ctypes.byref(st), self.batch, _raw_stream(stream)))
+        _check(lib().replayssm_check_device_errors(ctypes.byref(st), self.batch, _raw_stream(stream, self.work)))
 
 
 def conv_step(cs: ConvState, u, dt, out=None, stream=None, slots=None):
@@ -190,7 +206,7 @@ def conv_step(cs: ConvState, u, dt, out=None, stream=None, slots=None):
     rows = u.shape[0]
     d, st = cs._call(rows, slots)
     out, io = cs._io(u, dt, (rows,), out, stream)
-    _check(_lib().replayssm_conv_step(ctypes.byref(d), ctypes.byref(st), ctypes.byref(io), _raw_stream(stream)))
+    _check(_lib().replayssm_conv_step(ctypes.byref(d), ctypes.byref(st), ctypes.byref(io), _raw_stream(stream, u)))
     return out
 
 
@@ -201,7 +217,7 @@ def conv_verify(cs: ConvState, u, dt, out=None, stream=None, slots=None):
     rows, T = u.shape[:2]
     d, st = cs._call(rows, slots)
     out, io = cs._io(u, dt, (rows, T), out, stream)
-    _check(_lib().replayssm_conv_verify(ctypes.byref(d), ctypes.byref(st), T, ctypes.byref(io), _raw_stream(stream)))
+    _check(_lib().replayssm_conv_verify(ctypes.byref(d), ctypes.byref(st), T, ctypes.byref(io), _raw_stream(stream, u)))
     return out
 
 
@@ -210,7 +226,8 @@ def conv_accept(cs: ConvState, n_keep: torch.Tensor, T: int, stream=None, slots=
     rows = n_keep.numel()
     _need(n_keep, (rows,), torch.int32, "n_keep")
     d, st = cs._call(rows, slots)
-    _check(_lib().replayssm_conv_accept(ctypes.byref(d), ctypes.byref(st), n_keep.data_ptr(), T, _raw_stream(stream)))
+    _check(_lib().replayssm_conv_accept(ctypes.byref(d), ctypes.byref(st), n_keep.data_ptr(), T,
+                                        _raw_stream(stream, n_keep)))
 
 
 def _packed(cu_seqlens, fresh):
@@ -233,7 +250,7 @@ def conv_prefill(cs: ConvState, u, dt, cu_seqlens, *, from_zero: bool = False, f
     d, st = cs._call(rows, slots)
     out, io = cs._io(u, dt, (total,), out, stream)
     _check(_lib().replayssm_conv_prefill(ctypes.byref(d), ctypes.byref(st), total, cu_seqlens.data_ptr(),
-                                         int(from_zero), _ptr(fresh), ctypes.byref(io), _raw_stream(stream)))
+                                         int(from_zero), _ptr(fresh), ctypes.byref(io), _raw_stream(stream, u)))
     return out
 
 
@@ -283,14 +300,15 @@ def prefill_packed(ls: LayerState, x, B, C, dt, cu_seqlens, *, from_zero: bool =
     _check(L.replayssm_prefill_packed(ctypes.addressof(d), ctypes.addressof(st), total, cu_seqlens.data_ptr(),
                                       int(from_zero), _ptr(fresh), x.data_ptr(), B.data_ptr(), _ptr(C),
                                       dt.data_ptr(), _ptr(y), F32 if y is None else _TYPES[y.dtype],
-                                      _ptr(ws), need, _raw_stream(stream)))
+                                      _ptr(ws), need, _raw_stream(stream, x)))
     return y
 
 
 def _float(t, name):
-    if t.dtype not in _TYPES or not t.is_cuda:
+    ty = _TYPES.get(t.dtype)
+    if ty is None or not t.is_cuda:
         raise ReplaySSMError(f"{name}: expected an fp32 or bf16 device tensor, got {t.dtype} device={t.device}")
-    return _TYPES[t.dtype]
+    return ty
 
 
 def gated_norm(y, z, weight, *, groups: int = 1, eps: float = 1e-5, norm_before_gate: bool = False, out=None,
@@ -300,20 +318,21 @@ def gated_norm(y, z, weight, *, groups: int = 1, eps: float = 1e-5, norm_before_
     projection's rows), weight [dim] fp32; returns [rows,dim] in z's type."""
     if z.dim() != 2:
         raise ReplaySSMError(f"z: expected [rows, dim], got {tuple(z.shape)}")
-    rows, dim = z.shape
+    rows, dim = shape = z.shape
     yt, zt = _float(y, "y"), _float(z, "z")
     if y.shape[0] != rows or y.numel() != rows * dim or not y.is_contiguous():
         raise ReplaySSMError(f"y: expected a dense tensor of {rows} rows of {dim}, got {tuple(y.shape)} "
                              f"contiguous={y.is_contiguous()}")
     pitch = _pitch(z, (rows,), dim, z.dtype, "z")
-    _need(weight, (dim,), torch.float32, "weight")
+    w = _dense(weight, (dim,), torch.float32, "weight")
     if out is None:
-        out = _empty((rows, dim), z.dtype, z.device, stream)
-    else:
-        _need(out, (rows, dim), out.dtype, "out")
-    _check(_lib().replayssm_gated_norm(rows, dim, groups, y.data_ptr(), yt, z.data_ptr(), zt, pitch,
-                                       weight.data_ptr(), eps, int(norm_before_gate), out.data_ptr(),
-                                       _float(out, "out"), _raw_stream(stream)))
+        out = _empty(shape, z.dtype, z.device, stream)
+    ot = _float(out, "out")
+    rc = _lib().replayssm_gated_norm(rows, dim, groups, y.data_ptr(), yt, z.data_ptr(), zt, pitch, w, eps,
+                                     1 if norm_before_gate else 0, _dense(out, shape, out.dtype, "out"), ot,
+                                     _raw_stream(stream, z))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -325,22 +344,19 @@ def add_norm(x, residual, weight, *, scale: float = 1.0, post_weight=None, eps: 
     residual).  ``residual_out`` may be ``residual``."""
     if x.dim() != 2:
         raise ReplaySSMError(f"x: expected [rows, dim], got {tuple(x.shape)}")
-    rows, dim = x.shape
+    rows, dim = shape = x.shape
     xt, rt = _float(x, "x"), _float(residual, "residual")
-    _need(x, (rows, dim), x.dtype, "x")
-    _need(residual, (rows, dim), residual.dtype, "residual")
-    _need(weight, (dim,), torch.float32, "weight")
-    if post_weight is not None:
-        _need(post_weight, (dim,), torch.float32, "post_weight")
+    xp, rp = _dense(x, shape, x.dtype, "x"), _dense(residual, shape, residual.dtype, "residual")
+    w = _dense(weight, (dim,), torch.float32, "weight")
+    p = None if post_weight is None else _dense(post_weight, (dim,), torch.float32, "post_weight")
     if residual_out is None:
-        residual_out = _empty((rows, dim), residual.dtype, x.device, stream)
-    else:
-        _need(residual_out, (rows, dim), residual.dtype, "residual_out")
+        residual_out = _empty(shape, residual.dtype, x.device, stream)
     if out is None:
-        out = _empty((rows, dim), x.dtype, x.device, stream)
-    else:
-        _need(out, (rows, dim), out.dtype, "out")
-    _check(_lib().replayssm_add_norm(rows, dim, x.data_ptr(), xt, residual.data_ptr(), residual_out.data_ptr(), rt,
-                                     weight.data_ptr(), _ptr(post_weight), scale, eps, out.data_ptr(),
-                                     _float(out, "out"), _raw_stream(stream)))
+        out = _empty(shape, x.dtype, x.device, stream)
+    ot = _float(out, "out")
+    rc = _lib().replayssm_add_norm(rows, dim, xp, xt, rp, _dense(residual_out, shape, residual.dtype, "residual_out"),
+                                   rt, w, p, scale, eps, _dense(out, shape, out.dtype, "out"), ot,
+                                   _raw_stream(stream, x))
+    if rc:
+        _check(rc)
     return out, residual_out
