@@ -135,9 +135,9 @@ int check_unit(const char *what, int64_t rows, int32_t dim, int32_t groups, floa
     return RSSM_OK;
 }
 
-// Packed prompts run on the matrix cores where their operands are exact: bf16
-// inputs, and a state that is fp32 on both sides of the call.
-bool on_matrix_cores(const rssm_desc *d) { return d->in_dtype == RSSM_BF16 && split_mode(d) < 0; }
+// Packed prompts run on the matrix cores where the state is fp32 on both sides
+// of the call (a chunk of rows of as many heads must stay within 2 GiB).
+bool on_matrix_cores(const rssm_desc *d) { return split_mode(d) < 0 && d->n_heads <= 1 << 16; }
 
 }  // namespace
 
@@ -198,7 +198,7 @@ int replayssm_conv_prefill(const rssm_conv_desc *desc, const rssm_conv_state *st
 
 size_t replayssm_prefill_packed_workspace(const rssm_desc *desc, int64_t total) {
     if (check_desc(desc) != RSSM_OK || total < 0 || total > (int64_t)1 << 30 || !on_matrix_cores(desc)) return 0;
-    return rssm::scan_workspace(total, desc->n_heads, desc->n_groups);
+    return rssm::scan_workspace(total, desc->n_heads, desc->n_groups, desc->in_dtype == RSSM_BF16);
 }
 
 int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_t total,
@@ -230,7 +230,7 @@ int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_
     p.fresh = fresh;
     p.total = total;
     if (on_matrix_cores(desc))
-        return hip_status(rssm::launch_scan(p, y != nullptr, workspace, stream), "packed prefill launch");
+        return hip_status(rssm::launch_scan(p, desc->in_dtype == RSSM_BF16, y != nullptr, workspace, stream), "packed prefill launch");
     return hip_status(rssm::launch_prefill_packed(p, desc->in_dtype == RSSM_BF16, y != nullptr, split_mode(desc),
                                                   stream),
                       "packed prefill launch");

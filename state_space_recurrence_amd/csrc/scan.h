@@ -11,8 +11,9 @@ namespace rssm {
 constexpr int kScanChunk = 64;       // tokens per chunk
 
 // Heads per workgroup (of one B/C group): B and C are staged once for all of
-// them, and two chunks of four heads fill the LDS of a compute unit.
-inline int scan_heads(int hpg) { return hpg >= 3 ? 4 : hpg; }
+// them, and two chunks of four heads, or one of two heads in the three planes
+// of fp32 inputs, fill the LDS of a compute unit.
+inline int scan_heads(int hpg, bool in_bf16) { return in_bf16 ? (hpg >= 3 ? 4 : hpg) : (hpg >= 2 ? 2 : 1); }
 
 struct ScanParams {
     ReplayParams r;
@@ -30,8 +31,8 @@ struct ScanParams {
 // tokens together, 128 heads: 350 us so; cut twice or three times as fine the
 // pieces even out, the second launch takes 305 -> 290 us, but the first one
 // grows from 45 to 95 us.)
-inline int scan_segment(int64_t total, int H, int G) {
-    const int nh = scan_heads(H / G);
+inline int scan_segment(int64_t total, int H, int G, bool in_bf16) {
+    const int nh = scan_heads(H / G, in_bf16);
     const int64_t hb = (int64_t)G * ((H / G + nh - 1) / nh);
     const int64_t chunks = (total + kScanChunk - 1) / kScanChunk;
     const int64_t pieces = hb < 256 ? 256 / hb : 1;   // segments side by side
@@ -40,13 +41,12 @@ inline int scan_segment(int64_t total, int H, int G) {
     return (int)(per * kScanChunk);
 }
 
-inline size_t scan_workspace(int64_t total, int H, int G) {
-    const int64_t nfull = total / scan_segment(total, H, G);
+inline size_t scan_workspace(int64_t total, int H, int G, bool in_bf16) {
+    const int64_t nfull = total / scan_segment(total, H, G, in_bf16);
     return (size_t)nfull * H * (2 * 64 * 128 + 1) * sizeof(float);
 }
 
-// bf16 inputs, fp32 checkpoints.  p.loc etc. may be NULL when workspace is
-// absent: every sequence is then one segment.
-hipError_t launch_scan(const ReplayParams &p, bool outputs, void *workspace, hipStream_t s);
+// fp32 checkpoints.  Without a workspace every sequence is one segment.
+hipError_t launch_scan(const ReplayParams &p, bool in_bf16, bool outputs, void *workspace, hipStream_t s);
 
 }  // namespace rssm

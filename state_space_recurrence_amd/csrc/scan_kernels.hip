@@ -50,20 +50,21 @@ constexpr int kQ = kScanChunk;
 
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef float f2v __attribute__((ext_vector_type(2)));
+typedef unsigned int u2v __attribute__((ext_vector_type(2)));
 typedef int i8v __attribute__((ext_vector_type(8)));
 typedef int i4v __attribute__((ext_vector_type(4)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef short s8v __attribute__((ext_vector_type(8)));
 typedef __bf16 b2v __attribute__((ext_vector_type(2)));
 
-// NH heads and 2 NH waves a workgroup.
-template <int NH>
+// NH heads and 2 NH waves a workgroup; NP bf16 planes of each input.
+template <int NH, int NP>
 struct ScanSmem {
     struct Chunk {
-        alignas(16) char B[kQ][2 * kN];       // B_j[n]: 32-byte pair k of row j at k ^ (j mod 8)
-        alignas(16) char C[kQ][2 * kN];       // C_t[n], the same
-        alignas(16) char x[NH][kQ][2 * kP];   // x_j[p]: pair k of row j at k ^ (j / 2 mod 4)
-    } chunk[2];
+        alignas(16) char B[NP][kQ][2 * kN];       // B_j[n]: 32-byte pair k of row j at k ^ (j mod 8)
+        alignas(16) char C[NP][kQ][2 * kN];       // C_t[n], the same
+        alignas(16) char x[NP][NH][kQ][2 * kP];   // x_j[p]: pair k of row j at k ^ (j / 2 mod 4)
+    } chunk[NP == 1 ? 2 : 1];
     // per wave, with c_t / ln 2 = k_t + f_t, k_t whole and 0 <= f_t < 1:
     alignas(16) int k[2 * NH][kQ];
     alignas(16) float cf[2 * NH][kQ];         // dt_j 2^-f_j
@@ -241,11 +242,30 @@ __device__ __forceinline__ int segment_owner(const ScanParams &a, int j, int lan
     return lo;
 }
 
-// YP: bf16 parts of M and the state in y; OUT: outputs wanted; LOCAL: the
-// first launch, which leaves the end states of segments with a successor.
-template <typename TY, int YP, bool OUT, bool LOCAL, int NH>
-__global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
-    __shared__ ScanSmem<NH> sm;
+// Four consecutive floats as NP planes of four bf16; a non-finite value goes to
+// plane 0 alone.
+template <int NP>
+__device__ __forceinline__ void planes(f4v v, u2v (&part)[NP]) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            part[k][i] = __builtin_bit_cast(unsigned, __builtin_convertvector(f2v{v[2 * i], v[2 * i + 1]}, b2v));
+            const float r0 = v[2 * i] - __uint_as_float(part[k][i] << 16);
+            const float r1 = v[2 * i + 1] - __uint_as_float(part[k][i] & 0xFFFF0000u);
+            v[2 * i] = fabsf(r0) < __builtin_inff() ? r0 : 0.f;
+            v[2 * i + 1] = fabsf(r1) < __builtin_inff() ? r1 : 0.f;
+        }
+}
+
+// TIn: uint16_t (bf16) or float inputs; YP: bf16 parts of M, the state and fp32
+// inputs in y; OUT: outputs wanted; LOCAL: the first launch, which leaves the
+// end states of segments with a successor.
+template <typename TIn, typename TY, int YP, bool OUT, bool LOCAL, int NH>
+__global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1) scan_kernel(ScanParams a) {
+    constexpr int NP = sizeof(TIn) == 2 ? 1 : 3;
+    constexpr int NPY = NP == 1 ? 1 : YP;   // planes that count in y
+    __shared__ ScanSmem<NH, NP> sm;
     constexpr int kWaves = 2 * NH, kThreads = 64 * kWaves;
     const ReplayParams &r = a.r;
     const int lane = threadIdx.x & 63, c = lane & 31, hf = lane >> 5;
@@ -319,10 +339,10 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
         }
     }
 
-    const uint16_t *xin = reinterpret_cast<const uint16_t *>(r.x) + (size_t)tok0 * HP + (size_t)h * kP;
-    const uint16_t *Bin = reinterpret_cast<const uint16_t *>(r.Bm) + (size_t)tok0 * GN + (size_t)g * kN;
-    const uint16_t *Cin = reinterpret_cast<const uint16_t *>(r.Cm) + (size_t)tok0 * GN + (size_t)g * kN;
-    const uint16_t *dtin = reinterpret_cast<const uint16_t *>(r.dt) + (size_t)tok0 * r.H + h;
+    const TIn *xin = reinterpret_cast<const TIn *>(r.x) + (size_t)tok0 * HP + (size_t)h * kP;
+    const TIn *Bin = reinterpret_cast<const TIn *>(r.Bm) + (size_t)tok0 * GN + (size_t)g * kN;
+    const TIn *Cin = reinterpret_cast<const TIn *>(r.Cm) + (size_t)tok0 * GN + (size_t)g * kN;
+    const TIn *dtin = reinterpret_cast<const TIn *>(r.dt) + (size_t)tok0 * r.H + h;
     TY *yout = reinterpret_cast<TY *>(r.y) + (size_t)tok0 * HP + (size_t)h * kP + p0;
     const auto scalar = [](float v) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v))); };
     const float Ah = scalar(r.A[h]), Dh = scalar(r.D[h]);
@@ -331,8 +351,8 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
     // piece lane mod 16) or 8 rows of x (row lane / 8, piece lane mod 8).  The
     // chunk's first row is the (uniform) base; rows past the segment fall
     // outside the buffer resource and arrive as zeros.
-    const int bpitch = (int)GN * 2, xpitch = (int)HP * 2;
-    auto fetch = [&](int t0, int buf) {
+    const int bpitch = (int)GN * (int)sizeof(TIn), xpitch = (int)HP * (int)sizeof(TIn);
+    auto fetch16 = [&](int t0, int buf) {
         const int left = t0 < 0 || t0 > len ? 0 : (len - t0 < kQ ? len - t0 : kQ);
         const int rem = __builtin_amdgcn_readfirstlane(left);   // (a vector clamp would make the resources vector values)
         const u4v bs = resource_of(Bin + (size_t)t0 * GN, rem * bpitch);
@@ -346,21 +366,72 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
         for (int n = 0; n < 16 / kWaves; ++n) {   // rows 4 i + bl: an odd i turns the pairs by 4 more
             const int i = wave * (16 / kWaves) + n;
             const int off = (boff ^ (128 * (i & 1))) + 4 * i * bpitch;
-            load_to_lds(bs, off, lds_offset(ch.B[4 * i]));
-            if (OUT) load_to_lds(cs, off, lds_offset(ch.C[4 * i]));
+            load_to_lds(bs, off, lds_offset(ch.B[0][4 * i]));
+            if (OUT) load_to_lds(cs, off, lds_offset(ch.C[0][4 * i]));
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n) {   // a head's two waves take half of its rows each
             const int i = (wave & 1) * 4 + n;
-            load_to_lds(xs, xoff + 8 * i * xpitch, lds_offset(ch.x[hh][8 * i]));
+            load_to_lds(xs, xoff + 8 * i * xpitch, lds_offset(ch.x[0][hh][8 * i]));
+        }
+    };
+    // fp32 inputs: through registers, one chunk ahead, and split into planes on
+    // the way to LDS.  A thread takes pieces of four floats: 2048 of B and of C
+    // over the workgroup, 1024 of a head's x over its two waves.
+    constexpr int kBC = NP == 1 ? 1 : 2048 / kThreads, kX = NP == 1 ? 1 : 8;
+    f4v rB[kBC], rC[kBC], rX[kX];
+    auto fetch32 = [&](int t0) {
+        const int left = t0 < 0 || t0 > len ? 0 : (len - t0 < kQ ? len - t0 : kQ);
+        const int rem = __builtin_amdgcn_readfirstlane(left);
+        const auto bs = uniform_rsrc(Bin + (size_t)t0 * GN, rem * bpitch);
+        const auto cs = uniform_rsrc(Cin + (size_t)t0 * GN, OUT ? rem * bpitch : 0);
+        const auto xs = uniform_rsrc(xin + (size_t)t0 * HP, rem * xpitch);
+#pragma unroll
+        for (int n = 0; n < kBC; ++n) {
+            const int i = (int)threadIdx.x + n * kThreads, off = (i >> 5) * bpitch + 16 * (i & 31);
+            rB[n] = __builtin_amdgcn_raw_buffer_load_b128(bs, off, 0, 0);
+            if (OUT) rC[n] = __builtin_amdgcn_raw_buffer_load_b128(cs, off, 0, 0);
+        }
+#pragma unroll
+        for (int n = 0; n < kX; ++n) {
+            const int i = ((int)threadIdx.x & 127) + n * 128;
+            rX[n] = __builtin_amdgcn_raw_buffer_load_b128(xs, (i >> 4) * xpitch + 16 * (i & 15), 0, 0);
+        }
+    };
+    auto stage32 = [&]() {
+        auto &ch = sm.chunk[0];
+#pragma unroll
+        for (int n = 0; n < kBC; ++n) {
+            const int i = (int)threadIdx.x + n * kThreads, row = i >> 5, at = 32 * (((i >> 2) & 7) ^ (row & 7)) + 8 * (i & 3);
+            u2v part[NP];
+            planes<NP>(rB[n], part);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) *reinterpret_cast<u2v *>(&ch.B[k][row][at]) = part[k];
+            if (OUT) {
+                planes<NP>(rC[n], part);
+#pragma unroll
+                for (int k = 0; k < NPY; ++k) *reinterpret_cast<u2v *>(&ch.C[k][row][at]) = part[k];
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < kX; ++n) {
+            const int i = ((int)threadIdx.x & 127) + n * 128, row = i >> 4;
+            u2v part[NP];
+            planes<NP>(rX[n], part);
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                *reinterpret_cast<u2v *>(&ch.x[k][hh][row][32 * (((i >> 2) & 3) ^ ((row >> 1) & 3)) + 8 * (i & 3)]) = part[k];
         }
     };
     // dt of the lane's token in the chunk at t0
-    auto fetch_dt = [&](int t0) {
+    auto fetch_dt = [&](int t0) -> unsigned {
         const int left = t0 < 0 || t0 > len ? 0 : (len - t0 < kQ ? len - t0 : kQ);
-        const auto ds = uniform_rsrc(dtin + (size_t)t0 * r.H, __builtin_amdgcn_readfirstlane(left) * 2 * r.H);
-        return __builtin_amdgcn_raw_buffer_load_b16(ds, 2 * lane_again() * r.H, 0, 0);
+        const int pitch = r.H * (int)sizeof(TIn);
+        const auto ds = uniform_rsrc(dtin + (size_t)t0 * r.H, __builtin_amdgcn_readfirstlane(left) * pitch);
+        if constexpr (NP == 1) return __builtin_amdgcn_raw_buffer_load_b16(ds, lane_again() * pitch, 0, 0);
+        else return __builtin_amdgcn_raw_buffer_load_b32(ds, lane_again() * pitch, 0, 0);
     };
+
     // The first launch takes the chunks from the last to the first, each with
     // its decay to the segment's end (`total`): the accumulators are never
     // rescaled, and once a head's decay is exactly zero in fp32 its earlier
@@ -368,17 +439,18 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
     constexpr int kStep = LOCAL ? -kQ : kQ;
     const int t_first = LOCAL ? (len - 1) / kQ * kQ : 0;
     double total = 0.0;
-    fetch(t_first, 0);
+    if constexpr (NP == 1) fetch16(t_first, 0);
+    else fetch32(t_first);
     unsigned dt_bits = fetch_dt(t_first);
     int buf = 0;
-    for (int t0 = t_first; LOCAL ? t0 >= 0 : t0 < len; t0 += kStep, buf ^= 1) {
+    for (int t0 = t_first; LOCAL ? t0 >= 0 : t0 < len; t0 += kStep, buf ^= NP == 1) {
         const int q = len - t0 < kQ ? len - t0 : kQ;   // tokens of this chunk
         // The chunk has arrived (every wave waits for its own loads) and the
         // other buffer's reads are done: the next chunk goes there.
         const bool done = LOCAL && __builtin_amdgcn_exp2f((float)total) == 0.f;
         if (LOCAL && lane == 0) sm.done[buf][wave] = done;
         asm volatile("s_waitcnt vmcnt(0)" : "+v"(dt_bits)::"memory");   // (dt too: not waited for behind the next loads)
-        const float dt = __uint_as_float((uint32_t)dt_bits << 16);
+        const float dt = __uint_as_float(NP == 1 ? dt_bits << 16 : dt_bits);
         __syncthreads();
         if (LOCAL) {
             int all = 1;
@@ -386,7 +458,13 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
             for (int i = 0; i < kWaves; ++i) all &= sm.done[buf][i];
             if (__builtin_amdgcn_readfirstlane(all)) break;
         }
-        fetch(t0 + kStep, buf ^ 1);
+        if constexpr (NP == 1) {
+            fetch16(t0 + kStep, buf ^ 1);
+        } else {   // one buffer: its reads are done, and it is written before the next reads
+            stage32();
+            __syncthreads();
+            fetch32(t0 + kStep);
+        }
         if (LOCAL && done) {
             dt_bits = 0;
             continue;
@@ -405,7 +483,8 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
         const int get_x = 128 * tj + 32 * ((2 * (wave & 1) + tg) ^ ((tj >> 1) & 3)) + tc;       // + 2048 js
         const int get_y = 128 * col + 32 * ((2 * (wave & 1)) ^ ((col >> 1) & 3)) + 16 * half;   // row col of x: ^ 32 s
         const int yoff = (col * (int)HP + 8 * half) * (int)sizeof(TY);
-        const char *ldsB = sm.chunk[buf].B[0], *ldsC = sm.chunk[buf].C[0], *ldsX = sm.chunk[buf].x[hh][0];
+        const char *ldsB = sm.chunk[buf].B[0][0], *ldsC = sm.chunk[buf].C[0][0], *ldsX = sm.chunk[buf].x[0][hh][0];
+        constexpr int kPlane = 2 * kN * kQ, kPlaneX = 2 * kP * kQ * NH;   // bytes from plane to plane
 
         // ---- decays of the wave's head (both waves of a head compute them).
         // exp(c_t - c_j) = 2^(k_t - k_j) 2^f_t 2^-f_j: the fractions' powers
@@ -437,16 +516,31 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
                 b8v s[YP];
                 split<YP>(half_of(tile, ks & 1), s);
                 const int off = get_r ^ (32 * ks);
-                const b8v b0 = operand(ldsB + off), b1 = operand(ldsB + off + 32 * 256);
-                const b8v c0 = operand(ldsC + off), c1 = operand(ldsC + off + 32 * 256);
-                g00 = mfma(b0, c0, g00);
-                g01 = mfma(b0, c1, g01);
-                g11 = mfma(b1, c1, g11);
+                b8v c0[NPY], c1[NPY];
 #pragma unroll
-                for (int i = YP - 1; i >= 0; --i) {
-                    y0 = mfma(s[i], c0, y0);
-                    y1 = mfma(s[i], c1, y1);
+                for (int k = 0; k < NPY; ++k) {
+                    c0[k] = operand(ldsC + off + k * kPlane);
+                    c1[k] = operand(ldsC + off + k * kPlane + 32 * 256);
                 }
+                // of products of parts i and k, those with i + k < the number of parts count
+#pragma unroll
+                for (int k = NPY - 1; k >= 0; --k) {
+                    const b8v b0 = operand(ldsB + off + k * kPlane), b1 = operand(ldsB + off + k * kPlane + 32 * 256);
+#pragma unroll
+                    for (int i = NPY - 1 - k; i >= 0; --i) {
+                        g00 = mfma(b0, c0[i], g00);
+                        g01 = mfma(b0, c1[i], g01);
+                        g11 = mfma(b1, c1[i], g11);
+                    }
+                }
+#pragma unroll
+                for (int i = YP - 1; i >= 0; --i)
+#pragma unroll
+                    for (int k = NPY - 1; k >= 0; --k)
+                        if (i + k < YP) {
+                            y0 = mfma(s[i], c0[k], y0);
+                            y1 = mfma(s[i], c1[k], y1);
+                        }
             };
             step(st0, 0);
             step(st0, 1);
@@ -527,9 +621,12 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
                     }
                     b8v part[YP];
                     split<YP>(m, part);
-                    const b8v x = operand_t<128>(ldsX + get_x + 4096 * jt + 2048 * s);
 #pragma unroll
-                    for (int i = YP - 1; i >= 0; --i) y = mfma(x, part[i], y);
+                    for (int k = NPY - 1; k >= 0; --k) {
+                        const b8v x = operand_t<128>(ldsX + get_x + 4096 * jt + 2048 * s + k * kPlaneX);
+#pragma unroll
+                        for (int i = YP - 1 - k; i >= 0; --i) y = mfma(x, part[i], y);
+                    }
                 }
             };
             apply(g00, 0, k0, true, y0);
@@ -541,7 +638,11 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
             auto store = [&](const f16v &y, float rt, int tt) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    const f8v x = vec8<uint16_t>::widen(__builtin_bit_cast(u4u, operand(ldsX + (get_y ^ (32 * s)) + 32 * 128 * tt)));
+                    f8v x = vec8<uint16_t>::widen(__builtin_bit_cast(u4u, operand(ldsX + (get_y ^ (32 * s)) + 32 * 128 * tt)));
+#pragma unroll
+                    for (int k = 1; k < NPY; ++k)
+                        x += vec8<uint16_t>::widen(
+                            __builtin_bit_cast(u4u, operand(ldsX + (get_y ^ (32 * s)) + 32 * 128 * tt + k * kPlaneX)));
                     f8v v = half_of(y, s);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = fmaf(Dh, x[i], v[i] * rt);
@@ -562,7 +663,7 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
 
         __builtin_amdgcn_s_setprio(0);
         // the next chunk's dt, now that the accumulators of y and the Gram tiles are free
-        dt_bits = fetch_dt(t0 + kQ);
+        dt_bits = fetch_dt(t0 + kStep);
 
         // ---- S^T[n][p] = exp(c_63) S^T + sum_j B_j[n] (w_j x_j[p])
         if (!LOCAL)
@@ -576,20 +677,26 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
 #pragma unroll
         for (int js = 0; js < 4; ++js) {
             f8v v = vec8<uint16_t>::widen(__builtin_bit_cast(u4u, operand_t<128>(ldsX + get_x + 2048 * js)));
+#pragma unroll
+            for (int k = 1; k < NP; ++k)
+                v += vec8<uint16_t>::widen(__builtin_bit_cast(u4u, operand_t<128>(ldsX + get_x + 2048 * js + k * kPlaneX)));
             const f8v w = read8(&sm.w[wave][16 * js + row4]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= w[i];
             b8v part[3];
             split<3>(v, part);
-            const char *pb = ldsB + 4096 * js;
-            const b8v b0 = operand_t<256>(pb + get_b), b1 = operand_t<256>(pb + (get_b ^ 64)),
-                      b2 = operand_t<256>(pb + (get_b ^ 128)), b3 = operand_t<256>(pb + (get_b ^ 192));
 #pragma unroll
-            for (int i = 2; i >= 0; --i) {
-                st0 = mfma(b0, part[i], st0);
-                st1 = mfma(b1, part[i], st1);
-                st2 = mfma(b2, part[i], st2);
-                st3 = mfma(b3, part[i], st3);
+            for (int k = NP - 1; k >= 0; --k) {
+                const char *pb = ldsB + 4096 * js + k * kPlane;
+                const b8v b0 = operand_t<256>(pb + get_b), b1 = operand_t<256>(pb + (get_b ^ 64)),
+                          b2 = operand_t<256>(pb + (get_b ^ 128)), b3 = operand_t<256>(pb + (get_b ^ 192));
+#pragma unroll
+                for (int i = 2 - k; i >= 0; --i) {
+                    st0 = mfma(b0, part[i], st0);
+                    st1 = mfma(b1, part[i], st1);
+                    st2 = mfma(b2, part[i], st2);
+                    st3 = mfma(b3, part[i], st3);
+                }
             }
         }
         if (OUT && __builtin_amdgcn_ballot_w64(bad_row != 0) != 0) {
@@ -619,22 +726,22 @@ __global__ void __launch_bounds__(128 * NH, 2) scan_kernel(ScanParams a) {
     }
 }
 
-template <int NH>
+template <typename TIn, int NH>
 void launch_heads(const ScanParams &a, bool outputs, dim3 grid, hipStream_t s) {
     const dim3 block(128 * NH);
-    if (a.nfull) hipLaunchKernelGGL((scan_kernel<float, 3, false, true, NH>), grid, block, 0, s, a);
-    if (!outputs) hipLaunchKernelGGL((scan_kernel<float, 3, false, false, NH>), grid, block, 0, s, a);
-    else if (a.r.y_bf16) hipLaunchKernelGGL((scan_kernel<uint16_t, 2, true, false, NH>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((scan_kernel<float, 3, true, false, NH>), grid, block, 0, s, a);
+    if (a.nfull) hipLaunchKernelGGL((scan_kernel<TIn, float, 3, false, true, NH>), grid, block, 0, s, a);
+    if (!outputs) hipLaunchKernelGGL((scan_kernel<TIn, float, 3, false, false, NH>), grid, block, 0, s, a);
+    else if (a.r.y_bf16) hipLaunchKernelGGL((scan_kernel<TIn, uint16_t, 2, true, false, NH>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((scan_kernel<TIn, float, 3, true, false, NH>), grid, block, 0, s, a);
 }
 
 }  // namespace
 
-hipError_t launch_scan(const ReplayParams &p, bool outputs, void *workspace, hipStream_t s) {
+hipError_t launch_scan(const ReplayParams &p, bool in_bf16, bool outputs, void *workspace, hipStream_t s) {
     if (p.batch == 0 || p.total == 0) return hipSuccess;
     ScanParams a{};
     a.r = p;
-    a.lseg = scan_segment(p.total, p.H, p.G);
+    a.lseg = scan_segment(p.total, p.H, p.G, in_bf16);
     a.nfull = (int)(p.total / a.lseg);
     if (!workspace || a.nfull == 0) {   // one segment per sequence
         a.lseg = (int)((p.total + kScanChunk) / kScanChunk * kScanChunk);
@@ -645,15 +752,17 @@ hipError_t launch_scan(const ReplayParams &p, bool outputs, void *workspace, hip
         a.lam = a.s0 + (size_t)a.nfull * p.H * kP * kN;
     }
     a.nseg = (int)(p.total / a.lseg) + p.batch;
-    const int nh = scan_heads(p.H / p.G);
+    const int nh = scan_heads(p.H / p.G, in_bf16);
     a.hb = (p.H / p.G + nh - 1) / nh;
     a.r.wg_per_slot = p.G * a.hb;
     const int64_t blocks = ((int64_t)a.nseg * p.G + 7) / 8 * 8 * a.hb;
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks);
-    if (nh == 4) launch_heads<4>(a, outputs, grid, s);
-    else if (nh == 2) launch_heads<2>(a, outputs, grid, s);
-    else launch_heads<1>(a, outputs, grid, s);
+    if (nh == 4) launch_heads<uint16_t, 4>(a, outputs, grid, s);
+    else if (nh == 2 && in_bf16) launch_heads<uint16_t, 2>(a, outputs, grid, s);
+    else if (nh == 2) launch_heads<float, 2>(a, outputs, grid, s);
+    else if (in_bf16) launch_heads<uint16_t, 1>(a, outputs, grid, s);
+    else launch_heads<float, 1>(a, outputs, grid, s);
     return hipGetLastError();
 }
 

@@ -44,7 +44,7 @@ RSSM_STUB(hipError_t launch_conv_packed(const ConvParams &, bool, int, hipStream
 RSSM_STUB(hipError_t launch_conv_accept(const ConvParams &, hipStream_t))
 RSSM_STUB(hipError_t launch_gated_norm(const GatedNormParams &, bool, bool, bool, hipStream_t))
 RSSM_STUB(hipError_t launch_add_norm(const AddNormParams &, bool, bool, bool, hipStream_t))
-RSSM_STUB(hipError_t launch_scan(const ReplayParams &, bool, void *, hipStream_t))
+RSSM_STUB(hipError_t launch_scan(const ReplayParams &, bool, bool, void *, hipStream_t))
 RSSM_STUB(hipError_t launch_prefill_packed(const ReplayParams &, bool, bool, int, hipStream_t))
 }  // namespace rssm
 

@@ -251,7 +251,7 @@ SCAN_LENGTHS = [[0, 1, 15, 16, 17, 0, 63, 64, 65], [200], [1], [129, 0, 3], [255
 
 @pytest.mark.parametrize("lens", SCAN_LENGTHS)
 @pytest.mark.parametrize("H,G,dtype,ydt", [(4, 2, F32, F32), (3, 1, BF16, F32), (4, 2, BF16, BF16), (2, 2, BF16, F32),
-                                           (5, 1, F32, BF16)])
+                                           (5, 1, F32, BF16), (9, 1, BF16, F32)])
 def test_packed_prefill(rs, lens, H, G, dtype, ydt):
     g, n, slots, cu, fresh = _lens_case(lens, 21)
     ls, A, D, S0 = _layer(rs, n + 2, H, G, dtype, 31)
@@ -388,6 +388,76 @@ def test_no_rows_is_a_no_op(rs):
     y = rs.prefill_packed(ls, torch.empty(0, 2, 64, device="cuda"), torch.empty(0, 1, 128, device="cuda"),
                           torch.empty(0, 1, 128, device="cuda"), torch.empty(0, 2, device="cuda"), cu)
     assert y.shape == (0, 2, 64) and torch.equal(ls.ckpt.cpu(), S0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("what", ["x", "B", "C", "dt"])
+def test_packed_prefill_non_finite_inputs_stay_behind(rs, dtype, what):
+    """A non-finite value of a token reaches no earlier token of its sequence and no other sequence; a NaN in x stays
+    in its head's row of the state, and a C only in its own token."""
+    lens, H, G, bad = [70, 200, 64], 5, 1, 101      # token `bad` of the middle sequence, inside its second chunk
+    g, n, slots, cu, _ = _lens_case(lens, 27, 0)
+    ls, A, D, S0 = _layer(rs, n, H, G, dtype, 37)
+    ins = dict(zip(("x", "B", "C", "dt"), _scan_inputs(g, sum(lens), H, G, dtype)))
+    spoilt = {k: v.clone() for k, v in ins.items()}
+    at = 70 + bad
+    if what == "x":
+        spoilt["x"][at, 2, 37] = float("nan")
+        spoilt["x"][at + 3, 2, 5] = float("inf")
+    else:
+        spoilt[what][at] = float("nan")
+    y = rs.prefill_packed(ls, *(spoilt[k].cuda() for k in ("x", "B", "C", "dt")), cu.cuda(), slots=slots.cuda())
+    rs.check_device_errors(ls)
+    for r in range(n):
+        a, e, s = int(cu[r]), int(cu[r + 1]), int(slots[r])
+        yr, Sr, ym, Sm = ref.scan(S0[s], *(ins[k][a:e] for k in ("x", "B", "C", "dt")), A, D)
+        S = ls.ckpt[s]
+        if r != 1:
+            _check_scan(y[a:e], S, yr, Sr, ym, Sm, f"row {r}")
+            continue
+        _check_scan(y[a:at], torch.zeros_like(S), yr[:bad], torch.zeros_like(Sr), ym[:bad], Sm, "before")
+        rest = y[at:e].float().cpu()
+        if what == "x":
+            rows = torch.ones(H, 64, dtype=torch.bool)
+            rows[2, 37] = rows[2, 5] = False
+            ok = rows[None].expand(e - at, -1, -1)
+            tol = 2e-5 * yr[bad:].abs().clamp(min=1) + 64 * ref.U32 * ym[bad:]
+            assert ((rest.double() - yr[bad:]).abs()[ok] <= tol[ok]).all()
+            assert not torch.isfinite(rest[:, 2, 37]).any() and not torch.isfinite(rest[3:, 2, 5]).any()
+            assert torch.isfinite(rest[:3, 2, 5]).all()
+            Sg = S.cpu()
+            assert torch.isfinite(Sg[rows]).all() and not torch.isfinite(Sg[2, 37]).any()
+        elif what == "C":
+            assert torch.isnan(rest[0]).all() and torch.isfinite(rest[1:]).all()
+            ref.assert_within(S, Sr, 2e-5 * Sr.abs().clamp(min=1) + 64 * ref.U32 * Sm, "state")
+        else:
+            assert torch.isnan(rest).all()
+            assert torch.isnan(S).all()
+
+
+def test_packed_prefill_with_and_without_workspace(rs):
+    """Pieces run side by side and sequences run end to end agree to rounding."""
+    from state_space_recurrence_amd import mixer
+    import ctypes
+    lens, H, G = [1500, 3, 900], 4, 1
+    g, n, slots, cu, _ = _lens_case(lens, 29, 0)
+    ins = [t.cuda() for t in _scan_inputs(g, sum(lens), H, G, BF16)]
+    ins[3] = (ins[3].float() * 0.02).to(BF16)          # slow decays: earlier pieces reach into later ones
+    a, *_ = _layer(rs, n, H, G, BF16, 39)
+    b, *_ = _layer(rs, n, H, G, BF16, 39)
+    ya = rs.prefill_packed(a, *ins, cu.cuda())
+    d, st, _ = rs._ctx(b, None)
+    L = mixer._lib()
+    assert L.replayssm_prefill_packed_workspace(ctypes.addressof(d), sum(lens)) > 0
+    yb = torch.empty_like(ya)
+    x, B, C, dt = ins
+    c = cu.cuda()
+    rc = L.replayssm_prefill_packed(ctypes.addressof(d), ctypes.addressof(st), sum(lens), c.data_ptr(), 0, None,
+                                    x.data_ptr(), B.data_ptr(), C.data_ptr(), dt.data_ptr(), yb.data_ptr(), 0, None, 0,
+                                    torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    f = lambda u, v: float((u.double() - v.double()).norm() / v.double().norm())  # noqa: E731
+    assert f(ya, yb) < 2e-6 and f(a.ckpt, b.ckpt) < 2e-6
 
 
 def _decode_layer(rs, B, H, G, seed):

@@ -102,8 +102,8 @@ def test_packed_prefill_refuses(rs, m):
     assert ws(-1) == 0 and ws(0) == 0 and ws(1 << 31) == 0 and ws(100000) > 0
     assert L.replayssm_prefill_packed(A(d), A(st), 100000, 16, 0, None, 16, 16, 16, 16, 16, 0, 16, ws(100000) - 1,
                                       None) == -1 and b"workspace" in L.replayssm_last_error()
-    f = rs._make_desc(4, 8, 64, 128, 1, 16, 1, rs.F32)
-    assert L.replayssm_prefill_packed_workspace(A(f), 100000) == 0
+    low = rs._make_desc(4, 8, 64, 128, 1, 16, 1, rs.BF16, ckpt_dtype=rs.BF16, out_dtype=rs.FP4_E2M1)
+    assert L.replayssm_prefill_packed_workspace(A(low), 100000) == 0
 
 
 def test_norms_refuse(m):
