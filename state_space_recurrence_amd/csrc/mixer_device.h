@@ -25,6 +25,11 @@ template <> struct vec8<float> {
     static __device__ __forceinline__ raw8 load(const float *p) {
         return {*reinterpret_cast<const f4u *>(p), *reinterpret_cast<const f4u *>(p + 4)};
     }
+    // for data that is read once: does not displace what is in the caches
+    static __device__ __forceinline__ raw8 load_once(const float *p) {
+        return {__builtin_nontemporal_load(reinterpret_cast<const f4u *>(p)),
+                __builtin_nontemporal_load(reinterpret_cast<const f4u *>(p + 4))};
+    }
     static __device__ __forceinline__ raw8 zero() { return {(f4u)0.f, (f4u)0.f}; }
     static __device__ __forceinline__ void store_raw(float *p, const raw8 &r) {
         *reinterpret_cast<f4u *>(p) = r.a;
@@ -44,6 +49,9 @@ template <> struct vec8<float> {
 template <> struct vec8<uint16_t> {   // bf16, carried as its 16 bits
     typedef u4u raw8;
     static __device__ __forceinline__ raw8 load(const uint16_t *p) { return *reinterpret_cast<const u4u *>(p); }
+    static __device__ __forceinline__ raw8 load_once(const uint16_t *p) {
+        return __builtin_nontemporal_load(reinterpret_cast<const u4u *>(p));
+    }
     static __device__ __forceinline__ raw8 zero() { return (u4u)0u; }
     static __device__ __forceinline__ void store_raw(uint16_t *p, const raw8 &r) { *reinterpret_cast<u4u *>(p) = r; }
     static __device__ __forceinline__ f8v widen(const raw8 &r) {
@@ -63,20 +71,25 @@ template <> struct vec8<uint16_t> {   // bf16, carried as its 16 bits
     static __device__ __forceinline__ void put(uint16_t *p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 };
 
-// Up to eight elements at p, `left` of them inside the row (zeros past them).
-template <typename T>
+// Up to eight elements at p, `left` of them inside the row (zeros past them);
+// FULL: eight or none.
+template <bool FULL, typename T>
 __device__ __forceinline__ f8v load_part(const T *p, int left) {
-    if (left >= 8) return vec8<T>::widen(vec8<T>::load(p));
     f8v v = (f8v)0.f;
+    if constexpr (FULL) {
+        if (left > 0) v = vec8<T>::widen(vec8<T>::load(p));
+        return v;
+    }
+    if (left >= 8) return vec8<T>::widen(vec8<T>::load(p));
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < left) v[i] = vec8<T>::get(p + i);
     return v;
 }
 
-template <typename T>
+template <bool FULL, typename T>
 __device__ __forceinline__ void store_part(T *p, f8v v, int left) {
-    if (left >= 8) {
+    if (FULL || left >= 8) {
         vec8<T>::store(p, v);
         return;
     }
@@ -88,14 +101,6 @@ __device__ __forceinline__ void store_part(T *p, f8v v, int left) {
 // v sigmoid(v): the exponential overflows to infinity for large negative v,
 // whose reciprocal is the exact limit 0.
 __device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
-
-// Sum over the wave, in every lane; a fixed order.
-__device__ __forceinline__ float wave_sum(float v) {
-    v = row16_sum(v);
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    return v;
-}
 
 }  // namespace
 }  // namespace rssm

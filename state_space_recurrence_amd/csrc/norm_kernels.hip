@@ -15,13 +15,18 @@
 #include "mixer.h"
 #include "mixer_device.h"
 
+#include <type_traits>
+
 namespace rssm {
 namespace {
 
-// Sum over the THREADS lanes that share a unit (64: one wave).
+// Sum over the THREADS lanes that share a unit (32, 64, or a workgroup).
 template <int THREADS>
 __device__ __forceinline__ float unit_sum(float v, float *lds) {
-    v = wave_sum(v);
+    v = row16_sum(v);
+    v += __shfl_xor(v, 16);
+    if constexpr (THREADS == 32) return v;
+    v += __shfl_xor(v, 32);
     if constexpr (THREADS > 64) {
         __syncthreads();   // an earlier sum's reads are done
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
@@ -44,18 +49,18 @@ __device__ __forceinline__ float squares(const f8v (&v)[NV]) {
 }
 
 // THREADS lanes per unit, NV steps of eight elements a lane: units of up to
-// 8 THREADS NV elements.  A workgroup of 256 or more holds one unit, or four
-// units of one wave each.
-template <typename TY, typename TZ, typename TO, int THREADS, int NV>
+// 8 THREADS NV elements.  FULL: units are whole steps of eight (no tail code).
+// A workgroup of 256 or more holds one unit, or eight of half a wave each.
+template <typename TY, typename TZ, typename TO, int THREADS, int NV, bool FULL>
 __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) gated_norm_kernel(GatedNormParams p) {
     __shared__ float lds[16];
-    constexpr int kUnits = THREADS == 64 ? 4 : 1;
+    constexpr int kUnits = THREADS < 256 ? 256 / THREADS : 1;
     const int gsize = p.dim / p.groups;
-    const int64_t unit = (int64_t)blockIdx.x * kUnits + (THREADS == 64 ? threadIdx.x >> 6 : 0);
-    if (unit >= p.rows * p.groups) return;   // whole waves
+    const int64_t unit = (int64_t)blockIdx.x * kUnits + (kUnits > 1 ? threadIdx.x / THREADS : 0);
+    if (unit >= p.rows * p.groups) return;   // all lanes of the unit
     const int64_t row = unit / p.groups;
     const int c0 = (int)(unit - row * p.groups) * gsize;
-    const int lane = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
+    const int lane = kUnits > 1 ? threadIdx.x % THREADS : threadIdx.x;
     const TY *y = reinterpret_cast<const TY *>(p.y) + row * p.dim + c0;
     const TZ *z = reinterpret_cast<const TZ *>(p.z) + row * p.z_pitch + c0;
     TO *out = reinterpret_cast<TO *>(p.out) + row * p.dim + c0;
@@ -63,8 +68,8 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) gated_norm_kern
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = (k * THREADS + lane) * 8;
-        v[k] = load_part(y + c, gsize - c);
-        g[k] = load_part(z + c, gsize - c);
+        v[k] = load_part<FULL>(y + c, gsize - c);
+        g[k] = load_part<FULL>(z + c, gsize - c);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -78,24 +83,24 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) gated_norm_kern
     for (int k = 0; k < NV; ++k) {
         const int c = (k * THREADS + lane) * 8;
         if (c < gsize) {
-            f8v o = load_part(p.w + c0 + c, gsize - c);
+            f8v o = load_part<FULL>(p.w + c0 + c, gsize - c);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 o[i] = v[k][i] * r * o[i];
                 if (p.before) o[i] *= g[k][i];
             }
-            store_part(out + c, o, gsize - c);
+            store_part<FULL>(out + c, o, gsize - c);
         }
     }
 }
 
-template <typename TX, typename TR, typename TO, int THREADS, int NV>
+template <typename TX, typename TR, typename TO, int THREADS, int NV, bool FULL>
 __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) add_norm_kernel(AddNormParams p) {
     __shared__ float lds[16];
-    constexpr int kUnits = THREADS == 64 ? 4 : 1;
-    const int64_t row = (int64_t)blockIdx.x * kUnits + (THREADS == 64 ? threadIdx.x >> 6 : 0);
-    if (row >= p.rows) return;   // whole waves
-    const int lane = THREADS == 64 ? threadIdx.x & 63 : threadIdx.x;
+    constexpr int kUnits = THREADS < 256 ? 256 / THREADS : 1;
+    const int64_t row = (int64_t)blockIdx.x * kUnits + (kUnits > 1 ? threadIdx.x / THREADS : 0);
+    if (row >= p.rows) return;   // all lanes of the unit
+    const int lane = kUnits > 1 ? threadIdx.x % THREADS : threadIdx.x;
     const TX *x = reinterpret_cast<const TX *>(p.x) + row * p.dim;
     const TR *res = reinterpret_cast<const TR *>(p.res) + row * p.dim;
     TR *res_out = reinterpret_cast<TR *>(p.res_out) + row * p.dim;
@@ -104,15 +109,15 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) add_norm_kernel
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = (k * THREADS + lane) * 8;
-        v[k] = load_part(x + c, p.dim - c);
-        r[k] = load_part(res + c, p.dim - c);
+        v[k] = load_part<FULL>(x + c, p.dim - c);
+        r[k] = load_part<FULL>(res + c, p.dim - c);
     }
     if (p.post) {
         const float n = rsqrtf(unit_sum<THREADS>(squares(v), lds) / p.dim + p.eps);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (k * THREADS + lane) * 8;
-            const f8v w = load_part(p.post + c, p.dim - c);
+            const f8v w = load_part<FULL>(p.post + c, p.dim - c);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * n * w[i];
         }
@@ -126,44 +131,57 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) add_norm_kernel
     for (int k = 0; k < NV; ++k) {
         const int c = (k * THREADS + lane) * 8;
         if (c < p.dim) {
-            store_part(res_out + c, r[k], p.dim - c);
-            const f8v w = load_part(p.w + c, p.dim - c);
+            store_part<FULL>(res_out + c, r[k], p.dim - c);
+            const f8v w = load_part<FULL>(p.w + c, p.dim - c);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[k][i] = r[k][i] * n * w[i];
-            store_part(out + c, v[k], p.dim - c);
+            store_part<FULL>(out + c, v[k], p.dim - c);
         }
     }
 }
 
-template <typename F>
-hipError_t by_size(int n, F &&f) {
-    // lanes of a unit and steps of eight elements a lane
-    if (n <= 512) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-    else if (n <= 1024) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-    else if (n <= 2048) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
-    else if (n <= 4096) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
-    else if (n <= 8192) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
-    else if (n <= 16384) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
-    else return hipErrorInvalidValue;
+template <int TH, int NV, typename F>
+hipError_t by_tail(int n, F &&f) {
+    if (n % 8 == 0) f(std::integral_constant<int, TH>{}, std::integral_constant<int, NV>{}, std::true_type{});
+    else f(std::integral_constant<int, TH>{}, std::integral_constant<int, NV>{}, std::false_type{});
     return hipGetLastError();
 }
 
+// Lanes of a unit of n elements and steps of eight elements a lane.
+template <typename F>
+hipError_t by_size(int n, F &&f) {
+    if (n <= 256) return by_tail<32, 1>(n, f);
+    if (n <= 512) return by_tail<32, 2>(n, f);
+    if (n <= 768) return by_tail<32, 3>(n, f);
+    if (n <= 1024) return by_tail<32, 4>(n, f);
+    if (n <= 2048) return by_tail<256, 1>(n, f);
+    if (n <= 4096) return by_tail<256, 2>(n, f);
+    if (n <= 8192) return by_tail<1024, 1>(n, f);
+    if (n <= 16384) return by_tail<1024, 2>(n, f);
+    return hipErrorInvalidValue;
+}
+
+template <int TH>
+constexpr int kThreadsOf = TH < 256 ? 256 : TH;
+template <int TH>
+constexpr int kUnitsOf = TH < 256 ? 256 / TH : 1;
+
 template <typename TY, typename TZ, typename TO>
 hipError_t gated(const GatedNormParams &p, hipStream_t s) {
-    return by_size(p.dim / p.groups, [&](auto th, auto nv) {
+    return by_size(p.dim / p.groups, [&](auto th, auto nv, auto full) {
         constexpr int TH = decltype(th)::value, NV = decltype(nv)::value;
         const int64_t units = p.rows * p.groups;
-        const dim3 grid((unsigned)(TH == 64 ? (units + 3) / 4 : units)), block(TH == 64 ? 256 : TH);
-        hipLaunchKernelGGL((gated_norm_kernel<TY, TZ, TO, TH, NV>), grid, block, 0, s, p);
+        const dim3 grid((unsigned)((units + kUnitsOf<TH> - 1) / kUnitsOf<TH>)), block(kThreadsOf<TH>);
+        hipLaunchKernelGGL((gated_norm_kernel<TY, TZ, TO, TH, NV, decltype(full)::value>), grid, block, 0, s, p);
     });
 }
 
 template <typename TX, typename TR, typename TO>
 hipError_t added(const AddNormParams &p, hipStream_t s) {
-    return by_size(p.dim, [&](auto th, auto nv) {
+    return by_size(p.dim, [&](auto th, auto nv, auto full) {
         constexpr int TH = decltype(th)::value, NV = decltype(nv)::value;
-        const dim3 grid((unsigned)(TH == 64 ? (p.rows + 3) / 4 : p.rows)), block(TH == 64 ? 256 : TH);
-        hipLaunchKernelGGL((add_norm_kernel<TX, TR, TO, TH, NV>), grid, block, 0, s, p);
+        const dim3 grid((unsigned)((p.rows + kUnitsOf<TH> - 1) / kUnitsOf<TH>)), block(kThreadsOf<TH>);
+        hipLaunchKernelGGL((add_norm_kernel<TX, TR, TO, TH, NV, decltype(full)::value>), grid, block, 0, s, p);
     });
 }
 
