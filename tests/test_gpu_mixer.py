@@ -536,3 +536,17 @@ def test_calls_on_another_stream(rs):
 
     for a, b in zip(run(None), run(torch.cuda.Stream())):
         assert torch.equal(a, b)
+
+
+def test_example_stack(rs):
+    """The example: prompts at once, tokens and drafts against the same tokens one by one.  Every bf16 activation
+    between the parts may round the other way (2^-8 each; about ten of them in two blocks, growing with the square
+    root), outputs of both ways being right to fp32 before that."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "mixer_block.py")
+    spec = importlib.util.spec_from_file_location("mixer_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m.main(verbose=False) < 10 ** 0.5 * ref.U16
+    assert m.main(lengths=(300, 64, 2), tokens=3, seed=1, verbose=False) < 10 ** 0.5 * ref.U16
