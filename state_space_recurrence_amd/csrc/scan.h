@@ -21,8 +21,7 @@ struct ScanParams {
     float *s0;         // [nfull, H, P, N] copy of the start state of a split sequence (at its first segment's entry)
     float *lam;        // [nfull, H] decay over the segment
     int lseg;          // tokens per segment (a multiple of kScanChunk)
-    int nseg;          // segment entries in the grid: total / lseg + batch
-    int nfull;         // full segments that fit: total / lseg
+    int nfull;         // full segments that fit: total / lseg (the grid: these, then a rest per sequence)
     int hb;            // workgroups per (segment, group)
 };
 

@@ -226,20 +226,51 @@ __device__ __forceinline__ bool non_finite(b8v v) {
     return (bits & 0x80008000u) != 0;
 }
 
-// Last sequence s whose first segment entry, cu[s] / lseg + s, is <= j (the
-// entries of a sequence follow it; consecutive sequences never overlap).
-__device__ __forceinline__ int segment_owner(const ScanParams &a, int j, int lane) {
+// Full segment e of the call belongs to the last sequence that starts at or
+// before it, cu[s] / lseg <= e (of sequences with equal quotients only the last
+// can be a segment long, so no two claim the same e; some e have no segment).
+__device__ __forceinline__ int full_owner(const ScanParams &a, int e, int lane) {
     int lo = 0, n = a.r.batch;   // the answer is in lo .. lo + n - 1
     while (n > 1) {
         const int step = (n + 63) / 64;
         const int s = lo + lane * step;
-        const bool le = lane * step < n && a.r.cu[s] / a.lseg + s <= j;
+        const bool le = lane * step < n && a.r.cu[s] / a.lseg <= e;
         const uint64_t m = __ballot(le);
         const int k = m ? 63 - __builtin_clzll(m) : 0;
         n = n - k * step < step ? n - k * step : step;
         lo += k * step;
     }
     return lo;
+}
+
+// Sequences end in a rest shorter than a segment.  The j-th rest to run: of
+// each kRestBlock sequences the longest first, by eighths of a segment.
+constexpr int kRestBlock = 256;
+__device__ __forceinline__ int rest_owner(const ScanParams &a, int j, int lane) {
+    const int s0 = j / kRestBlock * kRestBlock;
+    j -= s0;
+    int cls[kRestBlock / 64];
+#pragma unroll
+    for (int i = 0; i < kRestBlock / 64; ++i) {
+        const int s = s0 + 64 * i + lane;
+        cls[i] = -1;
+        if (s < a.r.batch) {
+            const int len = (int)((unsigned)a.r.cu[s + 1] - (unsigned)a.r.cu[s]);
+            cls[i] = len > 0 ? (int)((unsigned)(len % a.lseg) / (unsigned)(a.lseg / 8)) : 0;
+        }
+    }
+    for (int c = 7; c >= 0; --c)
+#pragma unroll
+        for (int i = 0; i < kRestBlock / 64; ++i) {
+            const uint64_t m = __ballot(cls[i] == c);
+            const int n = __popcll(m);
+            if (j < n) {
+                const int rank = __builtin_amdgcn_mbcnt_hi((unsigned)(m >> 32), __builtin_amdgcn_mbcnt_lo((unsigned)m, 0));
+                return s0 + 64 * i + __builtin_ctzll(__ballot(cls[i] == c && rank == j));
+            }
+            j -= n;
+        }
+    return 0;   // not reached: every sequence has a class
 }
 
 // Four consecutive floats as NP planes of four bf16; a non-finite value goes to
@@ -278,19 +309,22 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
 
     // Workgroups of one (segment, group) read the same B and C: they follow
     // each other on one XCD, and the pairs are dealt to the XCDs in turn.
-    const int npair = a.nseg * r.G;
+    const int npair = (LOCAL ? a.nfull : a.nfull + r.batch) * r.G;
     const int xcd = blockIdx.x & 7, at = blockIdx.x >> 3;
     const int pair = (at / a.hb) * 8 + xcd, hblk = at % a.hb;
     if (pair >= npair) return;
     const int entry = pair / r.G, g = pair - entry * r.G;
 
-    const int seq = __builtin_amdgcn_readfirstlane(segment_owner(a, entry, lane));
+    // Full segments first, then the rests.
+    const bool full = entry < a.nfull;
+    const int seq = __builtin_amdgcn_readfirstlane(full ? full_owner(a, entry, lane) : rest_owner(a, entry - a.nfull, lane));
     const int start = __builtin_amdgcn_readfirstlane(r.cu[seq]), end = __builtin_amdgcn_readfirstlane(r.cu[seq + 1]);
     if (start < 0 || end > r.total || end <= start) return;
-    const int k = entry - (start / a.lseg + seq);
-    if (k < 0 || (int64_t)k * a.lseg >= end - start) return;
+    const int k = full ? entry - start / a.lseg : (end - start) / a.lseg;
+    if (k < 0 || (int64_t)(k + full) * a.lseg > end - start) return;
     const int tok0 = start + k * a.lseg;
-    const int len = end - tok0 < a.lseg ? end - tok0 : a.lseg;
+    const int len = full ? a.lseg : end - tok0;
+    if (len == 0) return;   // a sequence of whole segments has no rest
     const bool last = tok0 + len == end;
     if (LOCAL && last) return;
     const int b = __builtin_amdgcn_readfirstlane(slot_of_row(r, seq));
@@ -726,10 +760,15 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
     }
 }
 
+int64_t scan_blocks(const ScanParams &a, int segments) {   // of each (segment, group), in whole rounds over the XCDs
+    return ((int64_t)segments * a.r.G + 7) / 8 * 8 * a.hb;
+}
+
 template <typename TIn, int NH>
-void launch_heads(const ScanParams &a, bool outputs, dim3 grid, hipStream_t s) {
-    const dim3 block(128 * NH);
-    if (a.nfull) hipLaunchKernelGGL((scan_kernel<TIn, float, 3, false, true, NH>), grid, block, 0, s, a);
+void launch_heads(const ScanParams &a, bool outputs, hipStream_t s) {
+    const dim3 block(128 * NH), grid(scan_blocks(a, a.nfull + a.r.batch));
+    if (a.nfull)
+        hipLaunchKernelGGL((scan_kernel<TIn, float, 3, false, true, NH>), dim3(scan_blocks(a, a.nfull)), block, 0, s, a);
     if (!outputs) hipLaunchKernelGGL((scan_kernel<TIn, float, 3, false, false, NH>), grid, block, 0, s, a);
     else if (a.r.y_bf16) hipLaunchKernelGGL((scan_kernel<TIn, uint16_t, 2, true, false, NH>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((scan_kernel<TIn, float, 3, true, false, NH>), grid, block, 0, s, a);
@@ -751,18 +790,15 @@ hipError_t launch_scan(const ReplayParams &p, bool in_bf16, bool outputs, void *
         a.s0 = a.loc + (size_t)a.nfull * p.H * kP * kN;
         a.lam = a.s0 + (size_t)a.nfull * p.H * kP * kN;
     }
-    a.nseg = (int)(p.total / a.lseg) + p.batch;
     const int nh = scan_heads(p.H / p.G, in_bf16);
     a.hb = (p.H / p.G + nh - 1) / nh;
     a.r.wg_per_slot = p.G * a.hb;
-    const int64_t blocks = ((int64_t)a.nseg * p.G + 7) / 8 * 8 * a.hb;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    const dim3 grid((unsigned)blocks);
-    if (nh == 4) launch_heads<uint16_t, 4>(a, outputs, grid, s);
-    else if (nh == 2 && in_bf16) launch_heads<uint16_t, 2>(a, outputs, grid, s);
-    else if (nh == 2) launch_heads<float, 2>(a, outputs, grid, s);
-    else if (in_bf16) launch_heads<uint16_t, 1>(a, outputs, grid, s);
-    else launch_heads<float, 1>(a, outputs, grid, s);
+    if (scan_blocks(a, a.nfull + p.batch) > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (nh == 4) launch_heads<uint16_t, 4>(a, outputs, s);
+    else if (nh == 2 && in_bf16) launch_heads<uint16_t, 2>(a, outputs, s);
+    else if (nh == 2) launch_heads<float, 2>(a, outputs, s);
+    else if (in_bf16) launch_heads<uint16_t, 1>(a, outputs, s);
+    else launch_heads<float, 1>(a, outputs, s);
     return hipGetLastError();
 }
 

@@ -61,7 +61,7 @@ def _check_conv(got, out, err, dtv, dterr, dtype, H, G, what):
 
 @pytest.mark.parametrize("W,H,G,dtype,bias,act", [
     (4, 8, 1, BF16, True, "silu"), (3, 3, 3, F32, True, "silu"), (2, 6, 2, BF16, False, None),
-    (4, 5, 1, F32, False, "silu"), (4, 40, 2, BF16, True, "silu"),
+    (4, 5, 1, F32, False, "silu"), (4, 42, 2, BF16, True, "silu"),
 ])
 def test_conv_step_tokens(rs, W, H, G, dtype, bias, act):
     """Tokens one by one on a mapped pool with a padding row, over more tokens than the ring has rows."""
@@ -272,6 +272,31 @@ def test_packed_prefill(rs, lens, H, G, dtype, ydt):
     for s in untouched:
         assert torch.equal(ls.ckpt[s].cpu(), S0[s]) and int(ls.intv[s]) == 0
     assert int(ls.work.abs().sum()) == 0
+
+
+def test_packed_prefill_of_many_sequences(rs):
+    """Sequences of no, whole and broken segments, more of them than are put in order together: each runs once."""
+    g = _gen(61)
+    lens = torch.randint(0, 30, (520,), generator=g).tolist()
+    for at, n in ((3, 256), (100, 700), (255, 512), (256, 257), (400, 255), (519, 1030)):
+        lens[at] = n
+    H, G = 2, 1
+    g, n, slots, cu, fresh = _lens_case(lens, 62)
+    ls, A, D, S0 = _layer(rs, n + 2, H, G, BF16, 63)
+    x, B, C, dt = _scan_inputs(g, sum(lens), H, G, BF16)
+    y = rs.prefill_packed(ls, x.cuda(), B.cuda(), C.cuda(), dt.cuda(), cu.cuda(), fresh=fresh.cuda(), y_dtype=F32,
+                          slots=slots.cuda())
+    rs.check_device_errors(ls)
+    used = torch.zeros(n + 2, dtype=torch.int64)
+    used[slots.long()] = torch.tensor([int(v > 0) for v in lens])
+    assert torch.equal(ls.intv.cpu().long(), used)
+    for r in [3, 4, 99, 100, 101, 254, 255, 256, 257, 399, 400, 401, 518, 519]:
+        a, e, s = int(cu[r]), int(cu[r + 1]), int(slots[r])
+        if e == a:
+            continue
+        start = torch.zeros_like(S0[s]) if fresh[r] else S0[s]
+        yr, Sr, ym, Sm = ref.scan(start, x[a:e], B[a:e], C[a:e], dt[a:e], A, D)
+        _check_scan(y[a:e], ls.ckpt[s], yr, Sr, ym, Sm, f"row {r} of {e - a}")
 
 
 @pytest.mark.parametrize("fmt", ["split-bf16", "split-e4m3", "shared-fp4", "low-bf16", "low-e4m3"])
