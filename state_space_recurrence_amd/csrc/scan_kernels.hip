@@ -70,7 +70,12 @@ struct ScanSmem {
     alignas(16) float cf[2 * NH][kQ];         // dt_j 2^-f_j
     alignas(16) float w[2 * NH][kQ];          // dt_j exp(c_63 - c_j)
     float rf[2 * NH][kQ];                     // 2^f_t
-    int done[2][2 * NH];                      // per wave: nothing before the chunk counts (LOCAL)
+    union {
+        // G_tj = C_t . B_j of the lower tiles (t, j) = (0, 0), (1, 0), (1, 1) of 32 x 32, zero for j > t:
+        // piece q of 4 j of row t at q ^ (t mod 8)
+        alignas(16) float gram[3][32][32];
+        int done[2][2 * NH];                  // per wave: nothing before the chunk counts (LOCAL)
+    };
 };
 
 // Of each four quads the middle two trade places: row r of a 16-row tile
@@ -112,6 +117,10 @@ __device__ __forceinline__ void split(f8v v, b8v (&part)[NP]) {
 
 __device__ __forceinline__ f16v mfma(b8v a, b8v b, f16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f4v mfma16(b8v a, b8v b, f4v c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 __device__ __forceinline__ f8v half_of(const f16v &v, int s) {
@@ -386,16 +395,16 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
     // chunk's first row is the (uniform) base; rows past the segment fall
     // outside the buffer resource and arrive as zeros.
     const int bpitch = (int)GN * (int)sizeof(TIn), xpitch = (int)HP * (int)sizeof(TIn);
-    auto fetch16 = [&](int t0, int buf) {
-        const int left = t0 < 0 || t0 > len ? 0 : (len - t0 < kQ ? len - t0 : kQ);
-        const int rem = __builtin_amdgcn_readfirstlane(left);   // (a vector clamp would make the resources vector values)
+    auto rows_left = [&](int t0) {   // (a vector clamp would make the resources vector values)
+        return __builtin_amdgcn_readfirstlane(t0 < 0 || t0 > len ? 0 : (len - t0 < kQ ? len - t0 : kQ));
+    };
+    auto fetch_bc = [&](int t0, int buf) {
+        const int rem = rows_left(t0);
         const u4v bs = resource_of(Bin + (size_t)t0 * GN, rem * bpitch);
         const u4v cs = resource_of(Cin + (size_t)t0 * GN, OUT ? rem * bpitch : 0);
-        const u4v xs = resource_of(xin + (size_t)t0 * HP, rem * xpitch);
         auto &ch = sm.chunk[buf];
-        const int l = lane_again(), bl = l >> 4, xl = l >> 3;
+        const int l = lane_again(), bl = l >> 4;
         const int boff = bl * bpitch + 16 * ((l & 15) ^ (2 * bl));
-        const int xoff = xl * xpitch + 16 * ((l & 7) ^ (2 * ((xl >> 1) & 3)));
 #pragma unroll
         for (int n = 0; n < 16 / kWaves; ++n) {   // rows 4 i + bl: an odd i turns the pairs by 4 more
             const int i = wave * (16 / kWaves) + n;
@@ -403,8 +412,14 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
             load_to_lds(bs, off, lds_offset(ch.B[0][4 * i]));
             if (OUT) load_to_lds(cs, off, lds_offset(ch.C[0][4 * i]));
         }
+    };
+    auto fetch_x = [&](int t0, int buf, int n0, int n1) {
+        const u4v xs = resource_of(xin + (size_t)t0 * HP, rows_left(t0) * xpitch);
+        auto &ch = sm.chunk[buf];
+        const int l = lane_again(), xl = l >> 3;
+        const int xoff = xl * xpitch + 16 * ((l & 7) ^ (2 * ((xl >> 1) & 3)));
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {   // a head's two waves take half of its rows each
+        for (int n = n0; n < n1; ++n) {   // a head's two waves take half of its rows each
             const int i = (wave & 1) * 4 + n;
             load_to_lds(xs, xoff + 8 * i * xpitch, lds_offset(ch.x[0][hh][8 * i]));
         }
@@ -415,8 +430,7 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
     constexpr int kBC = NP == 1 ? 1 : 2048 / kThreads, kX = NP == 1 ? 1 : 8;
     f4v rB[kBC], rC[kBC], rX[kX];
     auto fetch32 = [&](int t0) {
-        const int left = t0 < 0 || t0 > len ? 0 : (len - t0 < kQ ? len - t0 : kQ);
-        const int rem = __builtin_amdgcn_readfirstlane(left);
+        const int rem = rows_left(t0);
         const auto bs = uniform_rsrc(Bin + (size_t)t0 * GN, rem * bpitch);
         const auto cs = uniform_rsrc(Cin + (size_t)t0 * GN, OUT ? rem * bpitch : 0);
         const auto xs = uniform_rsrc(xin + (size_t)t0 * HP, rem * xpitch);
@@ -459,9 +473,8 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
     };
     // dt of the lane's token in the chunk at t0
     auto fetch_dt = [&](int t0) -> unsigned {
-        const int left = t0 < 0 || t0 > len ? 0 : (len - t0 < kQ ? len - t0 : kQ);
         const int pitch = r.H * (int)sizeof(TIn);
-        const auto ds = uniform_rsrc(dtin + (size_t)t0 * r.H, __builtin_amdgcn_readfirstlane(left) * pitch);
+        const auto ds = uniform_rsrc(dtin + (size_t)t0 * r.H, rows_left(t0) * pitch);
         if constexpr (NP == 1) return __builtin_amdgcn_raw_buffer_load_b16(ds, lane_again() * pitch, 0, 0);
         else return __builtin_amdgcn_raw_buffer_load_b32(ds, lane_again() * pitch, 0, 0);
     };
@@ -473,9 +486,16 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
     constexpr int kStep = LOCAL ? -kQ : kQ;
     const int t_first = LOCAL ? (len - 1) / kQ * kQ : 0;
     double total = 0.0;
-    if constexpr (NP == 1) fetch16(t_first, 0);
-    else fetch32(t_first);
+    if constexpr (NP == 1) {
+        fetch_bc(t_first, 0);
+        fetch_x(t_first, 0, 0, 4);
+    } else fetch32(t_first);
     unsigned dt_bits = fetch_dt(t_first);
+    if (OUT)   // the quarters above the diagonal
+        for (int i = threadIdx.x; i < 128; i += kThreads) {
+            const int t = (i >> 2) & 15, q = 4 + (i & 3);
+            *reinterpret_cast<f4v *>(&sm.gram[2 * (i >> 6)][t][4 * (q ^ (t & 7))]) = (f4v)0.f;
+        }
     int buf = 0;
     for (int t0 = t_first; LOCAL ? t0 >= 0 : t0 < len; t0 += kStep, buf ^= NP == 1) {
         const int q = len - t0 < kQ ? len - t0 : kQ;   // tokens of this chunk
@@ -493,7 +513,8 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
             if (__builtin_amdgcn_readfirstlane(all)) break;
         }
         if constexpr (NP == 1) {
-            fetch16(t0 + kStep, buf ^ 1);
+            fetch_bc(t0 + kStep, buf ^ 1);
+            if (!OUT) fetch_x(t0 + kStep, buf ^ 1, 0, 4);   // (with outputs, between their products)
         } else {   // one buffer: its reads are done, and it is written before the next reads
             stage32();
             __syncthreads();
@@ -532,7 +553,9 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
             const float f = (float)(cum - whole);
             if (OUT) {
                 sm.k[wave][ln] = (int)whole;
-                sm.cf[wave][ln] = dt * __builtin_amdgcn_exp2f(-f);
+                // (from a non-finite dt on 2^f_t is NaN and y with it; its factor stays out of earlier tokens' 0 M)
+                const float cf = dt * __builtin_amdgcn_exp2f(-f);
+                sm.cf[wave][ln] = fabsf(cf) < __builtin_inff() ? cf : 0.f;
                 sm.rf[wave][ln] = __builtin_amdgcn_exp2f(f);
             }
             sm.w[wave][ln] = dt * __builtin_amdgcn_exp2f((float)(total + c63 - cum));   // (total: 0 but in LOCAL)
@@ -544,55 +567,117 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
 
         unsigned bad_row = 0;   // the lane's row has a non-finite x in this chunk
         if (OUT) {
-            // ---- y^T[p][t] = sum_n S[p][n] C_t[n] and the Gram tiles G^T[j][t] = B_j . C_t
-            f16v y0 = (f16v)0.f, y1 = (f16v)0.f, g00 = (f16v)0.f, g01 = (f16v)0.f, g11 = (f16v)0.f;
-            auto step = [&](const f16v &tile, int ks) {
-                b8v s[YP];
-                split<YP>(half_of(tile, ks & 1), s);
+            // ---- the Gram tiles, the same for every head: 10 pieces of 16 x 16 over the waves
+            const int get_g = 256 * (ln & 15) + 16 * ((ln >> 4) & 1) + 32 * ((ln >> 5) ^ (ln & 7));
+            b8v gb[4][NPY], gc[4][NPY];
+            auto get_gram = [&](int jt, int tt) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                    for (int k = 0; k < NPY; ++k) {
+                        gb[ks][k] = operand(ldsB + (get_g ^ (64 * ks)) + 4096 * jt + k * kPlane);
+                        gc[ks][k] = operand(ldsC + (get_g ^ (64 * ks)) + 4096 * tt + k * kPlane);
+                    }
+                if (NP == 1) __builtin_amdgcn_sched_barrier(0);
+            };
+            auto put_gram = [&](int jt, int tt) {
+                f4v g = (f4v)0.f;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+                    for (int k = NPY - 1; k >= 0; --k)
+#pragma unroll
+                        for (int i = NPY - 1 - k; i >= 0; --i) g = mfma16(gb[ks][k], gc[ks][i], g);
+                const int t = ln & 15, j = 4 * (ln >> 4);   // within the piece: the lane's t, its first j
+                if (jt == tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) g[i] = j + i <= t ? g[i] : 0.f;
+                *reinterpret_cast<f4v *>(&sm.gram[(tt >> 1) + (jt >> 1)][16 * (tt & 1) + t][4 * ((4 * (jt & 1) + (ln >> 4)) ^ (t & 7))]) = g;
+            };
+            for (int u = wave; u < 10; u += kWaves) {
+                const int tt = (u >= 1) + (u >= 3) + (u >= 6), jt = u - tt * (tt + 1) / 2;
+                if (NP == 1) get_gram(jt, tt);
+                if (u == wave) decays();   // while the operands come
+                if (NP != 1) get_gram(jt, tt);
+                put_gram(jt, tt);
+            }
+            // ---- y^T[p][t] = sum_n S[p][n] C_t[n]
+            f16v y0 = (f16v)0.f, y1 = (f16v)0.f;
+            b8v xr[4], cA[2][NPY], cB[2][NPY], sA[YP], sB[YP];   // operands of one step, and of the next
+            auto get_c = [&](int ks, b8v (&c)[2][NPY]) {
                 const int off = get_r ^ (32 * ks);
-                b8v c0[NPY], c1[NPY];
 #pragma unroll
                 for (int k = 0; k < NPY; ++k) {
-                    c0[k] = operand(ldsC + off + k * kPlane);
-                    c1[k] = operand(ldsC + off + k * kPlane + 32 * 256);
+                    c[0][k] = operand(ldsC + off + k * kPlane);
+                    c[1][k] = operand(ldsC + off + k * kPlane + 32 * 256);
                 }
-                // of products of parts i and k, those with i + k < the number of parts count
-#pragma unroll
-                for (int k = NPY - 1; k >= 0; --k) {
-                    const b8v b0 = operand(ldsB + off + k * kPlane), b1 = operand(ldsB + off + k * kPlane + 32 * 256);
-#pragma unroll
-                    for (int i = NPY - 1 - k; i >= 0; --i) {
-                        g00 = mfma(b0, c0[i], g00);
-                        g01 = mfma(b0, c1[i], g01);
-                        g11 = mfma(b1, c1[i], g11);
-                    }
-                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            // of products of parts i and k, those with i + k < the number of parts count
+            auto products = [&](const b8v (&part)[YP], const b8v (&c)[2][NPY]) {
 #pragma unroll
                 for (int i = YP - 1; i >= 0; --i)
 #pragma unroll
                     for (int k = NPY - 1; k >= 0; --k)
                         if (i + k < YP) {
-                            y0 = mfma(s[i], c0[k], y0);
-                            y1 = mfma(s[i], c1[k], y1);
+                            y0 = mfma(part[i], c[0][k], y0);
+                            y1 = mfma(part[i], c[1][k], y1);
                         }
             };
-            step(st0, 0);
-            step(st0, 1);
-            __builtin_amdgcn_sched_barrier(0);
-            step(st1, 2);
-            step(st1, 3);
-            __builtin_amdgcn_sched_barrier(0);
-            step(st2, 4);
-            step(st2, 5);
-            __builtin_amdgcn_sched_barrier(0);
-            step(st3, 6);
-            step(st3, 7);
-            decays();
-            // the Gram products stay here: moved down to their uses they would keep all their operands in registers
-            asm volatile("" : "+v"(g00), "+v"(g01), "+v"(g11));
-            __builtin_amdgcn_s_setprio(2);
+            // (between two products, a share of the next step's splitting)
+            auto mixed = [&]() {
+#pragma unroll
+                for (int i = 0; i < 2 * YP; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, YP == 2 ? 7 : 8, 0);
+                }
+                asm volatile("" : "+v"(y0), "+v"(y1));   // (no product is put off past its step)
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            get_c(0, cA);
+            split<YP>(half_of(st0, 0), sA);
+            // every wave's Gram pieces are in LDS (no wait for the next chunk's loads)
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            get_c(1, cB);
+            products(sA, cA);
+            split<YP>(half_of(st0, 1), sB);
+            mixed();
+            if constexpr (NP == 1) fetch_x(t0 + kStep, buf ^ 1, 0, 2);
+            get_c(2, cA);
+            products(sB, cB);
+            split<YP>(half_of(st1, 0), sA);
+            mixed();
+            get_c(3, cB);
+            products(sA, cA);
+            split<YP>(half_of(st1, 1), sB);
+            mixed();
+            if constexpr (NP == 1) fetch_x(t0 + kStep, buf ^ 1, 2, 4);
+            get_c(4, cA);
+            products(sB, cB);
+            split<YP>(half_of(st2, 0), sA);
+            mixed();
+            get_c(5, cB);
+            products(sA, cA);
+            split<YP>(half_of(st2, 1), sB);
+            mixed();
+            get_c(6, cA);
+            products(sB, cB);
+            split<YP>(half_of(st3, 0), sA);
+            mixed();
+            get_c(7, cB);
+            products(sA, cA);
+            split<YP>(half_of(st3, 1), sB);
+            mixed();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) xr[i] = operand(ldsX + (get_y ^ (32 * (i & 1))) + 32 * 128 * (i >> 1));
             const int k0 = sm.k[wave][col], k1 = sm.k[wave][32 + col];
             const float r0 = sm.rf[wave][col], r1 = sm.rf[wave][32 + col];
+            __builtin_amdgcn_sched_barrier(0);
+            products(sB, cB);
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd |= non_finite(xr[i]);
+            __builtin_amdgcn_s_setprio(2);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 y0[i] = __builtin_ldexpf(y0[i], k0);
@@ -602,9 +687,6 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
             // wave that meets one marks the outputs of its row from its token on,
             // notes the row for the state and takes the value out of its half of
             // x (which no other wave reads).
-            bool odd = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) odd |= non_finite(operand(ldsX + (get_y ^ (32 * (i & 1))) + 32 * 128 * (i >> 1)));
             const int upto = col - row4;
             if (__builtin_amdgcn_ballot_w64(odd) != 0) {
                 auto mark = [&](f16v &y, int from) {   // from: token of the lane less row4
@@ -640,32 +722,79 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
                     asm volatile("ds_write_b128 %0, %1" ::"v"((unsigned)(uintptr_t)(lds_char *)p), "v"(v) : "memory");
                 }
             }
-            // ---- y^T += x^T M^T without D and the factor 2^f_t, M^T as the operand straight from the Gram accumulators
-            auto apply = [&](const f16v &gram, int jt, int kt, bool diag, f16v &y) {
+            // ---- y^T += x^T M^T without D and the factor 2^f_t
+            const int get_m = 128 * col + 16 * (half ^ (col & 7));   // row col of a Gram tile: ^ 64 s, second half ^ 32
+            struct Factors {   // of 16 tokens j
+                f8v cf;
+                i8v kj;
+                b8v x[NPY];
+            } fA, fB;
+            f8v gA, gB;
+            auto get_f = [&](int js, Factors &f) {
+                f.cf = read8(&sm.cf[wave][16 * js + row4]);
+                f.kj = read8(&sm.k[wave][16 * js + row4]);
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const int j0 = 32 * jt + 16 * s + row4;
-                    f8v m = half_of(gram, s);
-                    const f8v cf = read8(&sm.cf[wave][j0]);
-                    const i8v kj = read8(&sm.k[wave][j0]);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        m[i] = __builtin_ldexpf(m[i] * cf[i], kt - kj[i]);
-                        if (diag) m[i] = 16 * s + 8 * (i >> 2) + (i & 3) <= upto ? m[i] : 0.f;
-                    }
-                    b8v part[YP];
-                    split<YP>(m, part);
-#pragma unroll
-                    for (int k = NPY - 1; k >= 0; --k) {
-                        const b8v x = operand_t<128>(ldsX + get_x + 4096 * jt + 2048 * s + k * kPlaneX);
-#pragma unroll
-                        for (int i = YP - 1 - k; i >= 0; --i) y = mfma(x, part[i], y);
-                    }
-                }
+                for (int k = 0; k < NPY; ++k) f.x[k] = operand_t<128>(ldsX + get_x + 2048 * js + k * kPlaneX);
             };
-            apply(g00, 0, k0, true, y0);
-            apply(g01, 0, k1, false, y1);
-            apply(g11, 1, k1, true, y1);
+            auto get_g8 = [&](int tile, int s) {
+                const char *gram = reinterpret_cast<const char *>(sm.gram[tile]);
+                const f4v a = *reinterpret_cast<const f4v *>(gram + (get_m ^ (64 * s))),
+                          b = *reinterpret_cast<const f4v *>(gram + (get_m ^ (64 * s + 32)));
+                return f8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            };
+            b8v mA[YP], mB[YP];
+            auto decayed = [&](f8v m, const Factors &f, int kt, b8v (&part)[YP]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m[i] = __builtin_ldexpf(m[i] * f.cf[i], kt - f.kj[i]);
+                split<YP>(m, part);
+            };
+            auto apply = [&](const b8v (&part)[YP], const Factors &f, f16v &y) {
+#pragma unroll
+                for (int k = NPY - 1; k >= 0; --k)
+#pragma unroll
+                    for (int i = YP - 1 - k; i >= 0; --i) y = mfma(f.x[k], part[i], y);
+            };
+            auto mixed_apply = [&]() {
+#pragma unroll
+                for (int i = 0; i < YP; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x2, 16, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            get_f(0, fA);
+            gA = get_g8(0, 0);
+            gB = get_g8(1, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            decayed(gA, fA, k0, mA);
+            __builtin_amdgcn_sched_barrier(0);
+            gA = get_g8(0, 1);
+            get_f(1, fB);
+            __builtin_amdgcn_sched_barrier(0);
+            apply(mA, fA, y0);
+            decayed(gB, fA, k1, mB);
+            mixed_apply();
+            gB = get_g8(1, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            apply(mB, fA, y1);
+            decayed(gA, fB, k0, mA);
+            mixed_apply();
+            gA = get_g8(2, 0);
+            get_f(2, fA);
+            __builtin_amdgcn_sched_barrier(0);
+            apply(mA, fB, y0);
+            decayed(gB, fB, k1, mB);
+            mixed_apply();
+            gB = get_g8(2, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            apply(mB, fB, y1);
+            get_f(3, fB);
+            decayed(gA, fA, k1, mA);
+            mixed_apply();
+            apply(mA, fA, y1);
+            decayed(gB, fB, k1, mB);
+            mixed_apply();
+            apply(mB, fB, y1);
             __builtin_amdgcn_s_setprio(1);
             // ---- out: y = 2^f_t y + D x; rows past the chunk (and an unseen head's) fall outside the resource
             const auto ys = uniform_rsrc(yout + (size_t)t0 * HP, live ? q * (int)HP * (int)sizeof(TY) : 0);
@@ -700,36 +829,94 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
         dt_bits = fetch_dt(t0 + kStep);
 
         // ---- S^T[n][p] = exp(c_63) S^T + sum_j B_j[n] (w_j x_j[p])
+        struct Weighted {
+            b8v x[NP];
+            f8v w;
+        } wA, wB;
+        struct Rows {
+            b8v b[4];
+        } rA, rB;
+        b8v pA[3], pB[3];
+        auto get_w = [&](int js, Weighted &f) {
+#pragma unroll
+            for (int k = 0; k < NP; ++k) f.x[k] = operand_t<128>(ldsX + get_x + 2048 * js + k * kPlaneX);
+            f.w = read8(&sm.w[wave][16 * js + row4]);
+        };
+        auto get_rows = [&](int js, int k, Rows &f) {
+            const char *pb = ldsB + 4096 * js + k * kPlane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f.b[i] = operand_t<256>(pb + (get_b ^ (64 * i)));
+        };
+        auto weigh = [&](const Weighted &f, b8v (&part)[3]) {
+            f8v v = vec8<uint16_t>::widen(__builtin_bit_cast(u4u, f.x[0]));
+#pragma unroll
+            for (int k = 1; k < NP; ++k) v += vec8<uint16_t>::widen(__builtin_bit_cast(u4u, f.x[k]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= f.w[i];
+            split<3>(v, part);
+        };
+        auto add = [&](int k, const b8v (&part)[3], const Rows &f) {
+#pragma unroll
+            for (int i = 2 - k; i >= 0; --i) {
+                st0 = mfma(f.b[0], part[i], st0);
+                st1 = mfma(f.b[1], part[i], st1);
+                st2 = mfma(f.b[2], part[i], st2);
+                st3 = mfma(f.b[3], part[i], st3);
+            }
+        };
+        auto mixed_add = [&]() {   // between two products, a share of the next tokens' weighing
+#pragma unroll
+            for (int i = 0; i < 12; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x2, 5, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        get_w(0, wA);
+        if constexpr (NP == 1) {
+            get_rows(0, 0, rA);
+            get_w(1, wB);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         if (!LOCAL)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            st0[i] *= lam;
-            st1[i] *= lam;
-            st2[i] *= lam;
-            st3[i] *= lam;
-        }
+            for (int i = 0; i < 16; ++i) {
+                st0[i] *= lam;
+                st1[i] *= lam;
+                st2[i] *= lam;
+                st3[i] *= lam;
+            }
+        weigh(wA, pA);
+        if constexpr (NP == 1) {
+            get_rows(1, 0, rB);
+            get_w(2, wA);
+            __builtin_amdgcn_sched_barrier(0);
+            add(0, pA, rA);
+            weigh(wB, pB);
+            mixed_add();
+            get_rows(2, 0, rA);
+            get_w(3, wB);
+            __builtin_amdgcn_sched_barrier(0);
+            add(0, pB, rB);
+            weigh(wA, pA);
+            mixed_add();
+            get_rows(3, 0, rB);
+            __builtin_amdgcn_sched_barrier(0);
+            add(0, pA, rA);
+            weigh(wB, pB);
+            mixed_add();
+            add(0, pB, rB);
+        } else {
 #pragma unroll
-        for (int js = 0; js < 4; ++js) {
-            f8v v = vec8<uint16_t>::widen(__builtin_bit_cast(u4u, operand_t<128>(ldsX + get_x + 2048 * js)));
+            for (int js = 0; js < 4; ++js) {
+                if (js) {
+                    get_w(js, wA);
+                    weigh(wA, pA);
+                }
 #pragma unroll
-            for (int k = 1; k < NP; ++k)
-                v += vec8<uint16_t>::widen(__builtin_bit_cast(u4u, operand_t<128>(ldsX + get_x + 2048 * js + k * kPlaneX)));
-            const f8v w = read8(&sm.w[wave][16 * js + row4]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= w[i];
-            b8v part[3];
-            split<3>(v, part);
-#pragma unroll
-            for (int k = NP - 1; k >= 0; --k) {
-                const char *pb = ldsB + 4096 * js + k * kPlane;
-                const b8v b0 = operand_t<256>(pb + get_b), b1 = operand_t<256>(pb + (get_b ^ 64)),
-                          b2 = operand_t<256>(pb + (get_b ^ 128)), b3 = operand_t<256>(pb + (get_b ^ 192));
-#pragma unroll
-                for (int i = 2 - k; i >= 0; --i) {
-                    st0 = mfma(b0, part[i], st0);
-                    st1 = mfma(b1, part[i], st1);
-                    st2 = mfma(b2, part[i], st2);
-                    st3 = mfma(b3, part[i], st3);
+                for (int k = NP - 1; k >= 0; --k) {
+                    get_rows(js, k, rA);
+                    add(k, pA, rA);
                 }
             }
         }
