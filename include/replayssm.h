@@ -384,7 +384,7 @@ int replayssm_conv_accept(const rssm_conv_desc *desc, const rssm_conv_state *st,
  * Packed prompts: row r holds tokens cu_seqlens[r] .. cu_seqlens[r+1]-1 of the
  * `total` packed tokens (cu_seqlens [batch+1] int32 device, ascending within
  * 0..total; offsets that do not are flagged, and what the call writes is then
- * undefined).  A row starts from its slot's history, or from zeros where
+ * undefined, work included: clear it with the state before they are used again).  A row starts from its slot's history, or from zeros where
  * fresh[r] != 0 (fresh [batch] int32 device; NULL: from_zero for every row).
  * The last W-1 inputs of history and prompt become the slot's history.  Rows
  * without tokens leave their slot as it is; tokens of no row are skipped.
@@ -406,13 +406,19 @@ int replayssm_conv_check_desc(const rssm_conv_desc *desc);
  * zero (fresh / from_zero as for replayssm_conv_prefill); the state after them
  * becomes the checkpoint (pos = 0, intv + 1).  Rows without tokens leave their
  * slot as it is.  Offsets that do not ascend within 0..total are flagged, and
- * what the call writes is then undefined.  Low-precision states as for replayssm_prefill.
+ * what the call writes is then undefined (work too: clear it with the state
+ * before either is used again).  Low-precision states as for replayssm_prefill.
+ * At most 32768 heads.
  * x [total,H,P], B, C [total,G,N], dt [total,H] (in_dtype); y [total,H,P] in
  * y_dtype (F32, or BF16 rounded once) or NULL (then C may be NULL).
  * workspace: device scratch (16-byte aligned) of at least
  * replayssm_prefill_packed_workspace bytes, which lets long sequences run in
  * parallel pieces, or NULL: every sequence is then run from end to end.  Its
  * contents are not kept between calls; calls that overlap need their own.
+ * fp32 states run on the matrix cores: a non-finite x makes its row of the
+ * state and of the outputs NaN from its token on (whatever the recurrence
+ * would make of it), and a token whose decay to the end of its sequence's
+ * piece is exactly 0 in fp32 leaves no trace behind that piece, finite or not.
  */
 int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_t total,
                              const int32_t *cu_seqlens, int32_t from_zero, const int32_t *fresh,

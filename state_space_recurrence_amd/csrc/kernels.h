@@ -76,8 +76,8 @@ hipError_t launch_load_f32(const ReplayParams &p, hipStream_t s);   // ckpt[slot
 hipError_t launch_defer_accept(const ReplayParams &p, hipStream_t s);
 // p.T = prompt length; mode -1 = fp32 checkpoint, else the SplitMode of a low-precision state
 hipError_t launch_prefill(const ReplayParams &p, bool in_bf16, bool outputs, int mode, hipStream_t s);
-// Packed prompts on the vector units: any input type and state format, one
-// head's chunks in sequence.
+// Packed prompts of low-precision states, on the vector units: a head's chunks
+// in sequence, rounded as launch_prefill rounds them.
 hipError_t launch_prefill_packed(const ReplayParams &p, bool in_bf16, bool outputs, int mode, hipStream_t s);
 hipError_t launch_split_step(const ReplayParams &p, bool in_bf16, int mode, hipStream_t s);
 hipError_t launch_split_verify(const ReplayParams &p, bool in_bf16, int mode, hipStream_t s);

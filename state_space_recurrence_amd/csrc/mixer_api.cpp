@@ -135,9 +135,8 @@ int check_unit(const char *what, int64_t rows, int32_t dim, int32_t groups, floa
     return RSSM_OK;
 }
 
-// Packed prompts run on the matrix cores where the state is fp32 on both sides
-// of the call (a chunk of rows of as many heads must stay within 2 GiB).
-bool on_matrix_cores(const rssm_desc *d) { return split_mode(d) < 0 && d->n_heads <= 1 << 16; }
+// Packed prompts run on the matrix cores where the state is fp32 on both sides of the call.
+bool on_matrix_cores(const rssm_desc *d) { return split_mode(d) < 0; }
 
 }  // namespace
 
@@ -208,6 +207,8 @@ int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_
     RSSM_TRY(check_desc(desc));
     if (total < 0 || total > (int64_t)1 << 30 || total * desc->n_heads > (int64_t)1 << 31)
         return fail(RSSM_E_ARG, "prefill_packed: total outside 0..2^30, or total * n_heads over 2^31");
+    if (desc->n_heads > 1 << 15)   // a chunk's rows are addressed in 31 bits
+        return fail(RSSM_E_CAPACITY, "prefill_packed: %d heads exceed 32768", desc->n_heads);
     if (from_zero != 0 && from_zero != 1) return fail(RSSM_E_ARG, "prefill_packed: from_zero must be 0 or 1");
     if (y && !float_type(y_dtype)) return fail(RSSM_E_UNSUPPORTED, "prefill_packed: y_dtype %d: F32 or BF16", y_dtype);
     RSSM_TRY(check_state(desc, st));

@@ -265,7 +265,10 @@ static hipError_t launch_prefill_any(const ReplayParams &p, bool in_bf16, bool o
                                      hipStream_t stream) {
     dim3 grid(p.batch * p.wg_per_slot), block(64 * p.hpw);
     switch (mode) {
-        case -1: launch_prefill_m<-1, PACKED>(p, in_bf16, outputs, grid, block, stream); break;
+        case -1:   // (packed prompts of fp32 states: launch_scan)
+            if constexpr (PACKED) return hipErrorInvalidValue;
+            else launch_prefill_m<-1, PACKED>(p, in_bf16, outputs, grid, block, stream);
+            break;
         case kSplitBF16: launch_prefill_m<kSplitBF16, PACKED>(p, in_bf16, outputs, grid, block, stream); break;
         case kSplitE4M3: launch_prefill_m<kSplitE4M3, PACKED>(p, in_bf16, outputs, grid, block, stream); break;
         case kSharedFP4: launch_prefill_m<kSharedFP4, PACKED>(p, in_bf16, outputs, grid, block, stream); break;

@@ -104,6 +104,8 @@ def test_packed_prefill_refuses(rs, m):
                                       None) == -1 and b"workspace" in L.replayssm_last_error()
     low = rs._make_desc(4, 8, 64, 128, 1, 16, 1, rs.BF16, ckpt_dtype=rs.BF16, out_dtype=rs.FP4_E2M1)
     assert L.replayssm_prefill_packed_workspace(A(low), 100000) == 0
+    wide = rs._make_desc(4, (1 << 15) + 1, 64, 128, 1, 16, 1, rs.BF16)
+    assert L.replayssm_prefill_packed(A(wide), A(st), 8, 16, 0, None, 16, 16, 16, 16, 16, 0, None, 0, None) == -3
 
 
 def test_norms_refuse(m):
