@@ -426,7 +426,7 @@ int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_
                              int32_t y_dtype, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Bytes of device scratch for a replayssm_prefill_packed call of `total`
- * tokens (0: none is used). */
+ * tokens with this descriptor (0: none is used). */
 size_t replayssm_prefill_packed_workspace(const rssm_desc *desc, int64_t total);
 
 /*

@@ -197,7 +197,7 @@ int replayssm_conv_prefill(const rssm_conv_desc *desc, const rssm_conv_state *st
 
 size_t replayssm_prefill_packed_workspace(const rssm_desc *desc, int64_t total) {
     if (check_desc(desc) != RSSM_OK || total < 0 || total > (int64_t)1 << 30 || !on_matrix_cores(desc)) return 0;
-    return rssm::scan_workspace(total, desc->n_heads, desc->n_groups, desc->in_dtype == RSSM_BF16);
+    return rssm::scan_workspace(total, desc->batch, desc->n_heads, desc->n_groups, desc->in_dtype == RSSM_BF16);
 }
 
 int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_t total,

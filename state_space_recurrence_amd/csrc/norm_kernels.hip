@@ -11,7 +11,14 @@
 //
 // Both are one pass over memory: a unit (a group, a row) is held in registers
 // between its sum of squares and its scaling, eight elements a lane and step.
-// Sums are fp32 in a fixed order.
+// Sums are fp32 in a fixed order; outputs are rounded once.
+//
+// Bound by memory.  Gated norm, 16384 rows of 6144 elements in 8 groups, bf16:
+// 123 us (604 MB, 4.9 TB/s); half a wave per group of 768 takes 123 us where a
+// wave of 64 took 131 and two waves 139, and one persistent workgroup per
+// compute unit that walks the rows 160 or more.  Add norm, 16384 rows of 4096,
+// bf16: 102 us (537 MB, 5.3 TB/s).  Single rows are bound by the launch: 256
+// rows of 6144 take 4.6 us, one row of 4096 2.5 to 3.3.
 #include "mixer.h"
 #include "mixer_device.h"
 

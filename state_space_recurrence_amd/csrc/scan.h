@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "kernels.h"
 
 namespace rssm {
@@ -27,21 +29,31 @@ struct ScanParams {
 
 // Tokens per segment for a call: long sequences are cut so that each of the
 // 256 compute units has a workgroup, and no finer.  (23 sequences of 9001
-// tokens together, 128 heads: 350 us so; cut twice or three times as fine the
-// pieces even out, the second launch takes 305 -> 290 us, but the first one
-// grows from 45 to 95 us.)
-inline int scan_segment(int64_t total, int H, int G, bool in_bf16) {
+// tokens together, 128 heads: in segments of half or a third of that the pieces
+// even out and the second launch loses 15 us, but the first one grows from 45
+// to 95 us.)
+//
+// Few heads would leave segments of a chunk or two.  A segment joins every one
+// before it, so n chunks are cut into no more than about 4 sqrt(n) segments; and
+// where twice the mean length is not five chunks (only the device knows the
+// lengths) segments keep at least four, as a launch more costs as much as two
+// chunks.  (8 heads: one sequence of 333 tokens in fp32 90 us in segments of four
+// chunks and 53 us in single ones, eight of together 2048 tokens of 16 heads in
+// bf16 71 and 64 us; five of together 200 tokens 30 us whole and 50 us cut.)
+inline int scan_segment(int64_t total, int batch, int H, int G, bool in_bf16) {
     const int nh = scan_heads(H / G, in_bf16);
     const int64_t hb = (int64_t)G * ((H / G + nh - 1) / nh);
     const int64_t chunks = (total + kScanChunk - 1) / kScanChunk;
     const int64_t pieces = hb < 256 ? 256 / hb : 1;   // segments side by side
     int64_t per = (chunks + pieces - 1) / pieces;
-    if (per < 4) per = 4;
+    const int64_t likely = batch > 2 ? 2 * total / batch : total;
+    const int64_t least = likely > 4 * kScanChunk ? (int64_t)std::ceil(std::sqrt((double)chunks / 16.0)) : 4;
+    if (per < least) per = least;
     return (int)(per * kScanChunk);
 }
 
-inline size_t scan_workspace(int64_t total, int H, int G, bool in_bf16) {
-    const int64_t nfull = total / scan_segment(total, H, G, in_bf16);
+inline size_t scan_workspace(int64_t total, int batch, int H, int G, bool in_bf16) {
+    const int64_t nfull = total / scan_segment(total, batch, H, G, in_bf16);
     return (size_t)nfull * H * (2 * 64 * 128 + 1) * sizeof(float);
 }
 

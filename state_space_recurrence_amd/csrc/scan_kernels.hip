@@ -1,5 +1,5 @@
 // scan_kernels.hip -- packed prompts through the recurrence on the matrix
-// cores (bf16 inputs, fp32 checkpoints).
+// cores (bf16 or fp32 inputs, fp32 checkpoints).
 //
 // A sequence is taken in chunks of 64 tokens.  With l_i = A dt_i, c_t the sum
 // of l over the chunk up to t, and S the state before the chunk:
@@ -11,8 +11,11 @@
 // for the whole segment.  An accumulator holds 4 consecutive rows per lane
 // half, an operand 8 consecutive inner indices; which n or p a row stands for,
 // and the order of the inner index, are free as long as both sides agree, so
-// accumulators (the state for S C, the decayed Gram tile for M x) are the next
-// product's operands straight from registers.
+// the state's accumulators are the operands of S C straight from registers.
+// The Gram tiles C B^T are the same for every head: the workgroup's waves form
+// them in pieces of 16 x 16, zero above the diagonal, and share them in LDS
+// (each wave forming all of them costs 24 more matrix instructions a chunk and
+// the 48 registers that the next step's operands now take).
 //
 // Staging.  The chunk's B, C and x go from memory to LDS directly (16 bytes a
 // lane, no registers), one chunk ahead in the other of two buffers; rows of B
@@ -30,6 +33,22 @@
 // whose own rounding is 2^-8.  Decay sums run in fp64 and are kept as a whole
 // and a fractional power of two: a difference of two long sums would
 // otherwise lose the bits of a short one.
+//
+// What bounds it.  One sequence of 16384 tokens, 96 heads in 8 groups, bf16:
+// 33 us for the first launch and 195 us for the second while the clock holds
+// (240 us in long runs), where 473 MB would take 96 us at the copy rate.  Of a
+// chunk's 15000 cycles a SIMD's two waves need 6400 for matrix instructions,
+// and each wave 5500 to issue its 1250 vector instructions (most of them split
+// the state and M into parts).  A wave issues one instruction at a time, so
+// what counts is that neither products nor LDS reads are waited for: operands
+// are read a step ahead, and the next step's vector work stands between the
+// products of the last (without both 214 us, with the reads alone 205).  More
+// than two waves a SIMD would need more than the LDS: a chunk is 64 KB, twice.
+// With fp32 outputs a chunk takes 122 products instead of 98, and 20000 cycles.
+//
+// Order.  Whole segments run first, then the sequences' rests by falling
+// length: 23 sequences of 9001 tokens together, 128 heads, fp32 outputs, take
+// 254 us a call so and 283 us in the sequences' own order.
 //
 // Long sequences.  When sequences x heads do not fill the card, a sequence is
 // cut into segments: a first launch leaves each segment's end state (the first
@@ -967,7 +986,7 @@ hipError_t launch_scan(const ReplayParams &p, bool in_bf16, bool outputs, void *
     if (p.batch == 0 || p.total == 0) return hipSuccess;
     ScanParams a{};
     a.r = p;
-    a.lseg = scan_segment(p.total, p.H, p.G, in_bf16);
+    a.lseg = scan_segment(p.total, p.batch, p.H, p.G, in_bf16);
     a.nfull = (int)(p.total / a.lseg);
     if (!workspace || a.nfull == 0) {   // one segment per sequence
         a.lseg = (int)((p.total + kScanChunk) / kScanChunk * kScanChunk);
