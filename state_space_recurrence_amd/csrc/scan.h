@@ -31,7 +31,10 @@ struct ScanParams {
 // 256 compute units has a workgroup, and no finer.  (23 sequences of 9001
 // tokens together, 128 heads: in segments of half or a third of that the pieces
 // even out and the second launch loses 15 us, but the first one grows from 45
-// to 95 us.)
+// to 95 us.)  Where there are sequences enough for that, a segment may be a
+// third longer: a sequence not much above the mean load is then not cut for the
+// price of a first launch (the same, over six sets of lengths: 256 us in
+// segments of the mean load, 237 us a third longer, 246 us half as long again).
 //
 // Few heads would leave segments of a chunk or two.  A segment joins every one
 // before it, so n chunks are cut into no more than about 4 sqrt(n) segments; and
@@ -46,6 +49,7 @@ inline int scan_segment(int64_t total, int batch, int H, int G, bool in_bf16) {
     const int64_t chunks = (total + kScanChunk - 1) / kScanChunk;
     const int64_t pieces = hb < 256 ? 256 / hb : 1;   // segments side by side
     int64_t per = (chunks + pieces - 1) / pieces;
+    if (batch >= pieces) per += per / 3;   // sequences fill the card by themselves
     const int64_t likely = batch > 2 ? 2 * total / batch : total;
     const int64_t least = likely > 4 * kScanChunk ? (int64_t)std::ceil(std::sqrt((double)chunks / 16.0)) : 4;
     if (per < least) per = least;
