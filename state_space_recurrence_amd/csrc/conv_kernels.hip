@@ -269,23 +269,21 @@ __global__ void __launch_bounds__(kThreads) conv_packed_kernel(ConvParams p) {
                         V::store_raw(ring + (size_t)wrap(q.head + q.m - 1 - k, p.R) * p.Cc, V::zero());
             }
         }
-        // Publish the heads of the sequences of which this tile holds the
-        // first token or one of the kept ones (the tiles that read the head
-        // or write ring rows).
+        // Publish the heads of the sequences whose history this tile read or
+        // wrote, the last of their tiles to arrive does.
         __syncthreads();
         if (threadIdx.x == 0) {
             for (int k = s0; k <= s; ++k) {
                 const int start = p.cu[k], end = p.cu[k + 1];
                 if (start < 0 || end <= start || end > p.total) continue;
-                const int m = end - start < W - 1 ? end - start : W - 1;
-                const int ta = start / p.tile, tb = (end - m) / p.tile, tc = (end - 1) / p.tile;
-                if (tile != ta && tile != tb && tile != tc) continue;
+                const HistoryTiles tiles(start, end, W, p.tile);
+                if (!tiles.has(tile)) continue;
                 const int b = p.slot_idx ? p.slot_idx[k] : k;
                 if (b < 0 || b >= p.nslots) continue;
-                const int tiles = 1 + (tb != ta) + (tc != tb && tc != ta);
+                const int m = end - start < W - 1 ? end - start : W - 1;
                 int head = p.head[b];   // not published before this arrival
                 head = head < 0 || head >= p.R ? 0 : head;
-                arrive(p, b, tiles * p.nblk, wrap(head + m, p.R));
+                arrive(p, b, tiles.count() * p.nblk, wrap(head + m, p.R));
             }
         }
     }
@@ -342,8 +340,8 @@ hipError_t launch_conv_packed(const ConvParams &p0, bool in_bf16, int width, hip
     ConvParams p = p0;
     p.nblk = (p.Cc / kVec + kThreads - 1) / kThreads;
     // 32 tokens a workgroup read 3 of their neighbour's again; when that leaves
-    // compute units without work, fewer tokens do (down to 4: a sequence's
-    // last inputs then lie in two tiles at most).
+    // compute units without work, fewer tokens do (down to 4, more than the
+    // W - 1 that HistoryTiles asks for).
     p.tile = 32;
     while (p.tile > 4 && (p.total + p.tile - 1) / p.tile * p.nblk < 512) p.tile >>= 1;
     const dim3 grid((unsigned)((p.total + p.tile - 1) / p.tile * p.nblk)), block(kThreads);

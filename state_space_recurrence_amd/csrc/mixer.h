@@ -33,6 +33,27 @@ struct ConvParams {
     int tile;               // packed prompts: tokens per workgroup
 };
 
+// Packed prompts go over tiles of tokens.  The tiles that touch a slot's history
+// for the prompt start .. end - 1 (end > start): that of the first token and that
+// of the last token whose taps reach before the prompt read it (the head, and ring
+// rows behind it), those of the last W - 1 inputs, which are kept, write it.  With
+// tiles of at least W - 1 tokens no other tile holds a token between the ends of
+// either pair, so the new head may be published when all of these are done.
+struct HistoryTiles {
+    int first, reach, keep, last;   // not descending, but for keep, which may lie before reach
+    __host__ __device__ HistoryTiles(int start, int end, int width, int tile) {
+        const int m = end - start < width - 1 ? end - start : width - 1;   // tokens that reach back, and inputs kept
+        first = start / tile;
+        reach = (start + m - 1) / tile;
+        keep = (end - m) / tile;
+        last = (end - 1) / tile;
+    }
+    __host__ __device__ bool has(int t) const { return t == first || t == reach || t == keep || t == last; }
+    __host__ __device__ int count() const {
+        return 1 + (reach != first) + (keep != first && keep != reach) + (last != first && last != reach && last != keep);
+    }
+};
+
 hipError_t launch_conv_tokens(const ConvParams &p, bool in_bf16, int width, bool advance, hipStream_t s);
 hipError_t launch_conv_packed(const ConvParams &p, bool in_bf16, int width, hipStream_t s);
 hipError_t launch_conv_accept(const ConvParams &p, hipStream_t s);
