@@ -254,26 +254,13 @@ def conv_prefill(cs: ConvState, u, dt, cu_seqlens, *, from_zero: bool = False, f
     return out
 
 
-def _workspace(ls: LayerState, need: int, device, stream):
-    """The layer's scratch, kept between calls and grown when a call needs more.
-    Calls on one layer are ordered, so they can share it; a stream other than
-    the one it was allocated on is noted with the allocator."""
-    at = torch.cuda.current_stream() if stream is None else stream
-    ws, home = getattr(ls, "_packed_ws", (None, None))
-    if ws is None or ws.numel() < need:
-        ws, home = _empty((need,), torch.uint8, device, at), at.cuda_stream
-        ls._packed_ws = (ws, home)
-    elif home != at.cuda_stream:
-        ws.record_stream(at)
-    return ws
-
-
 def prefill_packed(ls: LayerState, x, B, C, dt, cu_seqlens, *, from_zero: bool = False, fresh=None,
                    outputs: bool = True, y=None, y_dtype: torch.dtype = torch.float32, stream=None, slots=None):
     """Packed prompts into the checkpoints (replayssm_prefill_packed): x
     [total,H,P], B/C [total,G,N], dt [total,H], cu_seqlens [rows+1] int32 device
     offsets; returns y [total,H,P] in ``y_dtype`` (fp32 or bf16; of ``y`` when it
-    is given) when ``outputs``, else None."""
+    is given) when ``outputs``, else None.  A call allocates its scratch, as it
+    does a missing ``y``, and gives it back to the allocator."""
     rows, total = _packed(cu_seqlens, fresh), x.shape[0]
     if slots is None and rows != ls.batch:
         raise ReplaySSMError(f"a call without slots covers all {ls.batch} slots, got {rows} sequences")
@@ -296,7 +283,9 @@ def prefill_packed(ls: LayerState, x, B, C, dt, cu_seqlens, *, from_zero: bool =
         y = None
     L = _lib()
     need = L.replayssm_prefill_packed_workspace(ctypes.addressof(d), total)
-    ws = _workspace(ls, need, x.device, stream) if need else None
+    # Scratch of this call alone, from its own stream's memory (or a capture's): calls of one layer on two streams
+    # share nothing, a captured call's stays with its graph, and no layer holds any between calls.
+    ws = _empty((need,), torch.uint8, x.device, stream) if need else None
     _check(L.replayssm_prefill_packed(ctypes.addressof(d), ctypes.addressof(st), total, cu_seqlens.data_ptr(),
                                       int(from_zero), _ptr(fresh), x.data_ptr(), B.data_ptr(), _ptr(C),
                                       dt.data_ptr(), _ptr(y), F32 if y is None else _TYPES[y.dtype],
