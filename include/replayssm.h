@@ -417,8 +417,9 @@ int replayssm_conv_check_desc(const rssm_conv_desc *desc);
  * contents are not kept between calls; calls that overlap need their own.
  * fp32 states run on the matrix cores: a non-finite x makes its row of the
  * state and of the outputs NaN from its token on (whatever the recurrence
- * would make of it), and a token whose decay to the end of its sequence's
- * piece is exactly 0 in fp32 leaves no trace behind that piece, finite or not.
+ * would make of it).  A state value that is not finite stays so to the end of
+ * its sequence, and its row's outputs with it, however fast the state decays
+ * and with or without a workspace.
  */
 int replayssm_prefill_packed(const rssm_desc *desc, const rssm_state *st, int64_t total,
                              const int32_t *cu_seqlens, int32_t from_zero, const int32_t *fresh,

@@ -20,8 +20,11 @@ inline int scan_heads(int hpg, bool in_bf16) { return in_bf16 ? (hpg >= 3 ? 4 : 
 struct ScanParams {
     ReplayParams r;
     float *loc;        // [nfull, H, P, N] end state of each full segment that has a successor
-    float *s0;         // [nfull, H, P, N] copy of the start state of a split sequence (at its first segment's entry)
+    float *s0;         // [nfull, H, P, N] copy of the start state of a split sequence (at its first segment's entry);
+                       // behind the second launch, the end state of each marked half of a head
     float *lam;        // [nfull, H] decay over the segment
+    int *mark;         // [nfull, H, 2] end state not all finite, in the head's lower and upper 32 rows
+    int *marked;       // [1] any mark set
     int lseg;          // tokens per segment (a multiple of kScanChunk)
     int nfull;         // full segments that fit: total / lseg (the grid: these, then a rest per sequence)
     int hb;            // workgroups per (segment, group)
@@ -58,7 +61,7 @@ inline int scan_segment(int64_t total, int batch, int H, int G, bool in_bf16) {
 
 inline size_t scan_workspace(int64_t total, int batch, int H, int G, bool in_bf16) {
     const int64_t nfull = total / scan_segment(total, batch, H, G, in_bf16);
-    return (size_t)nfull * H * (2 * 64 * 128 + 1) * sizeof(float);
+    return nfull ? ((size_t)nfull * H * (2 * 64 * 128 + 3) + 1) * sizeof(float) : 0;
 }
 
 // fp32 checkpoints.  Without a workspace every sequence is one segment.

@@ -55,8 +55,12 @@
 // from the slot's state, the others from zero), and in the second every
 // segment joins the states before it, S = loc_{k-1} + lam_{k-1} (loc_{k-2} +
 // ...), before it runs its tokens.  Both sums end where the decay is exactly
-// zero in fp32: what lies before cannot change them (nor can a non-finite
-// value there, which a token by token recurrence would carry on).
+// zero in fp32: what lies before cannot change them, unless it is not finite,
+// which the recurrence carries on (0 NaN is NaN) however fast the state decays.
+// The second launch passes every token, so there each segment marks an end
+// state that is not all finite, and a third launch, of a workgroup per segment
+// and eight heads, puts NaN where the marked states say (where none is marked,
+// the call takes 2.5 us longer for it).
 #include "device_common.h"
 #include "mixer_device.h"
 #include "replay_common.h"
@@ -334,6 +338,8 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
     if (!LOCAL && blockIdx.x == 0)   // offsets that do not ascend (the mapping below stays within the tensors)
         for (int i = threadIdx.x; i <= r.batch; i += kThreads)
             if (r.cu[i] < 0 || r.cu[i] > r.total || (i && r.cu[i] < r.cu[i - 1])) atomicOr(r.err, kErrSeq);
+
+    if (LOCAL && blockIdx.x == 0 && threadIdx.x == 0) *a.marked = 0;
 
     // Workgroups of one (segment, group) read the same B and C: they follow
     // each other on one XCD, and the pairs are dealt to the XCDs in turn.
@@ -963,6 +969,72 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
     } else if (last) {
         if (live) put_state(ckpt);
         publish_position(r, b, 0, true, -1);
+    } else if (live) {
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            odd |= !(fabsf(st0[i]) < __builtin_inff()) || !(fabsf(st1[i]) < __builtin_inff()) ||
+                   !(fabsf(st2[i]) < __builtin_inff()) || !(fabsf(st3[i]) < __builtin_inff());
+        const size_t e = (ent0 + k) * r.H + h;
+        const bool mark = __builtin_amdgcn_ballot_w64(odd) != 0;
+        if (mark) put_state(a.s0 + e * headN);   // (the copy of the start state there has been read)
+        if (lane == 0) {
+            a.mark[2 * e + (wave & 1)] = mark;
+            if (mark) *a.marked = 1;
+        }
+    }
+}
+
+// The piece behind full segment `entry`, eight heads of it: rows whose state was
+// not finite at the end of any of the sequence's segments so far get NaN outputs,
+// and where the piece is the last one the state's elements get NaN.
+constexpr int kMarkHeads = 8;
+
+template <typename TY>
+__global__ void __launch_bounds__(256) carry_non_finite_kernel(ScanParams a) {
+    if (*a.marked == 0) return;
+    __shared__ int bad[kP];
+    const ReplayParams &r = a.r;
+    const int nblk = (r.H + kMarkHeads - 1) / kMarkHeads;
+    const int entry = blockIdx.x / nblk, h0 = (blockIdx.x - entry * nblk) * kMarkHeads;
+    const int h1 = h0 + kMarkHeads < r.H ? h0 + kMarkHeads : r.H;
+    const int seq = full_owner(a, entry, threadIdx.x & 63);
+    const int start = r.cu[seq], end = r.cu[seq + 1];
+    if (start < 0 || end > r.total || end <= start) return;
+    const int ent0 = start / a.lseg, k = entry - ent0;
+    if (k < 0 || (int64_t)(k + 1) * a.lseg >= end - start) return;   // no such segment, or nothing behind it
+    const int b = slot_of_row(r, seq);
+    if (b < 0) return;   // padding row
+    const int per = 2 * (h1 - h0);   // marks of a segment
+    int any = 0;
+    for (int i = threadIdx.x; i < (k + 1) * per; i += 256)
+        any |= a.mark[2 * ((size_t)(ent0 + i / per) * r.H + h0) + i % per];
+    if (!__syncthreads_or(any)) return;
+
+    const int tok0 = start + (k + 1) * a.lseg;
+    const int len = end - tok0 < a.lseg ? end - tok0 : a.lseg;
+    const bool last = tok0 + len == end;
+    for (int h = h0; h < h1; ++h) {
+        if (threadIdx.x < kP) bad[threadIdx.x] = 0;
+        __syncthreads();
+        float *ckpt = r.ckpt + ((size_t)b * r.H + h) * (kP * kN);
+        for (int i = 0; i <= k; ++i) {
+            const size_t e = (size_t)(ent0 + i) * r.H + h;
+            for (int half = 0; half < 2; ++half)
+                if (a.mark[2 * e + half])
+                    for (int at = half * 32 * kN + threadIdx.x; at < (half + 1) * 32 * kN; at += 256)
+                        if (!(fabsf(a.s0[e * (kP * kN) + at]) < __builtin_inff())) {
+                            bad[at / kN] = 1;
+                            if (last && fabsf(ckpt[at]) < __builtin_inff()) ckpt[at] = __builtin_nanf("");
+                        }
+        }
+        __syncthreads();
+        if (r.y) {
+            TY *y = reinterpret_cast<TY *>(r.y) + ((size_t)tok0 * r.H + h) * kP;
+            for (int64_t i = threadIdx.x; i < (int64_t)len * kP; i += 256)
+                if (bad[i % kP]) vec8<TY>::put(y + i / kP * ((size_t)r.H * kP) + i % kP, __builtin_nanf(""));
+        }
+        __syncthreads();
     }
 }
 
@@ -978,6 +1050,10 @@ void launch_heads(const ScanParams &a, bool outputs, hipStream_t s) {
     if (!outputs) hipLaunchKernelGGL((scan_kernel<TIn, float, 3, false, false, NH>), grid, block, 0, s, a);
     else if (a.r.y_bf16) hipLaunchKernelGGL((scan_kernel<TIn, uint16_t, 2, true, false, NH>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((scan_kernel<TIn, float, 3, true, false, NH>), grid, block, 0, s, a);
+    if (!a.nfull) return;
+    const dim3 marks(a.nfull * ((a.r.H + kMarkHeads - 1) / kMarkHeads));
+    if (a.r.y_bf16) hipLaunchKernelGGL(carry_non_finite_kernel<uint16_t>, marks, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(carry_non_finite_kernel<float>, marks, dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -995,6 +1071,8 @@ hipError_t launch_scan(const ReplayParams &p, bool in_bf16, bool outputs, void *
         a.loc = static_cast<float *>(workspace);
         a.s0 = a.loc + (size_t)a.nfull * p.H * kP * kN;
         a.lam = a.s0 + (size_t)a.nfull * p.H * kP * kN;
+        a.mark = reinterpret_cast<int *>(a.lam + (size_t)a.nfull * p.H);
+        a.marked = a.mark + (size_t)a.nfull * p.H * 2;
     }
     const int nh = scan_heads(p.H / p.G, in_bf16);
     a.hb = (p.H / p.G + nh - 1) / nh;

@@ -1,9 +1,13 @@
 """Packed prefill in the settings of a server: captured graphs, several
 streams, and inputs at which the pieces of a long sequence meet."""
+import ctypes
+
 import pytest
 import torch
 
-from test_gpu_mixer import BF16, _gen, _layer, _lens_case, _scan_inputs, rs  # noqa: F401
+import mixer_ref as ref
+from state_space_recurrence_amd import mixer
+from test_gpu_mixer import BF16, F32, _gen, _layer, _lens_case, _scan_inputs, rs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +77,69 @@ def test_prefills_of_one_layer_on_two_streams(rs):  # noqa: F811
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
         assert torch.equal(one.ckpt, two.ckpt), i
     rs.check_device_errors(two)
+
+
+def _whole(rs, ls, x, B, C, dt, cu, y):  # noqa: F811
+    """The packed call without scratch: every sequence in one piece."""
+    d, st, _ = rs._ctx(ls, None)
+    rc = mixer._lib().replayssm_prefill_packed(
+        ctypes.addressof(d), ctypes.addressof(st), x.shape[0], cu.data_ptr(), 0, None, x.data_ptr(), B.data_ptr(),
+        C.data_ptr(), dt.data_ptr(), y.data_ptr(), 1 if y.dtype == BF16 else 0, None, 0,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+
+
+@pytest.mark.parametrize("what", ["x", "B", "C", "dt", "start"])
+@pytest.mark.parametrize("dtype,ydt,lens", [(BF16, BF16, [4000]), (F32, F32, [2100]), (BF16, F32, [900, 5, 1500, 64])])
+def test_non_finite_values_cross_the_pieces(rs, dtype, ydt, lens, what):  # noqa: F811
+    """A NaN stays in the state and in all later outputs of its sequence however many pieces the sequence is cut into
+    and however fast the state decays: the same elements as when each sequence runs in one piece, which is what the
+    recurrence makes of them (0 NaN is NaN)."""
+    H, G, q = 9, 1, 0 if len(lens) == 1 else 2
+    g, n, _, cu, _ = _lens_case(lens, 91, 0)
+    x, B, C, dt = _scan_inputs(g, sum(lens), H, G, dtype)
+    a, A, D, S0 = _layer(rs, n, H, G, dtype, 93)
+    b, *_ = _layer(rs, n, H, G, dtype, 93)
+    at, end = int(cu[q]) + 33, int(cu[q + 1])
+    state, rows = torch.zeros(H, 64, 128, dtype=torch.bool), torch.zeros(H, 64, dtype=torch.bool)   # which are NaN
+    if what == "x":
+        x[at, 2, 37] = float("nan")
+        x[at, 8, 0] = float("nan")
+        rows[2, 37] = rows[8, 0] = True
+        state |= rows[..., None]
+    elif what == "B":
+        B[at, 0, 100] = float("nan")
+        state[:, :, 100] = True
+        rows[:] = True
+    elif what == "C":
+        C[at] = float("nan")
+    elif what == "dt":
+        dt[at, 4] = float("nan")
+        state[4] = rows[4] = True
+    else:
+        for ls in (a, b):
+            ls.ckpt[q, 5, 40, 7] = float("nan")
+        state[5, 40, 7] = rows[5, 40] = True
+        at = int(cu[q])
+    ins, cug = [t.cuda() for t in (x, B, C, dt)], cu.cuda()
+    assert mixer._lib().replayssm_prefill_packed_workspace(ctypes.addressof(rs._ctx(a, None)[0]), sum(lens)) > 0
+    y = rs.prefill_packed(a, *ins, cug, y_dtype=ydt)
+    yw = torch.empty_like(y)
+    _whole(rs, b, *ins, cug, yw)
+    rs.check_device_errors(a)
+    nan_y = torch.zeros(sum(lens), H, 64, dtype=torch.bool)
+    nan_y[at:end] = rows
+    if what == "C":
+        nan_y[at] = True
+    nan_S = torch.zeros(n, H, 64, 128, dtype=torch.bool)
+    nan_S[q] = state
+    for way, got_y, got_S in (("whole", yw, b.ckpt), ("in pieces", y, a.ckpt)):
+        assert torch.equal(torch.isnan(got_S).cpu(), nan_S), way
+        assert torch.equal(torch.isnan(got_y).cpu(), nan_y), way
+    # what is finite is right
+    near = lambda u, v, t: float((u - v).nan_to_num().norm() / v.nan_to_num().norm()) < t  # noqa: E731
+    assert near(a.ckpt, b.ckpt, 2e-6) and near(y.float(), yw.float(), 2e-6 if ydt == F32 else ref.U16)
+    a.ckpt.zero_()
+    rs.prefill_packed(a, ins[0], ins[1], None, ins[3], cug, outputs=False)
+    if what != "start":
+        assert torch.equal(torch.isnan(a.ckpt).cpu(), nan_S)
