@@ -573,7 +573,10 @@ __global__ void __launch_bounds__(128 * NH, sizeof(TIn) == 2 && NH == 4 ? 2 : 1)
         auto decays = [&]() {
             float A = Ah;
             asm volatile("" : "+s"(A));   // (its product is not held in vector registers)
-            const double cum = prefix((double)A * 1.4426950408889634 * (double)dt), whole = __builtin_floor(cum);
+            // (a token's decay below 2^-2^20 is zero either way; kept there, the whole parts of 64 tokens fit an int)
+            double log2a = (double)A * 1.4426950408889634 * (double)dt;
+            log2a = log2a < -0x1p20 && fabsf(dt) < __builtin_inff() ? -0x1p20 : log2a;
+            const double cum = prefix(log2a), whole = __builtin_floor(cum);
             const double c63 = lane_d(cum, 63);
             const float f = (float)(cum - whole);
             if (OUT) {

@@ -7,7 +7,7 @@ import torch
 
 import mixer_ref as ref
 from state_space_recurrence_amd import mixer
-from test_gpu_mixer import BF16, F32, _gen, _layer, _lens_case, _scan_inputs, rs  # noqa: F401
+from test_gpu_mixer import BF16, F32, _check_scan, _gen, _layer, _lens_case, _scan_inputs, rs  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,18 @@ def test_non_finite_values_cross_the_pieces(rs, dtype, ydt, lens, what):  # noqa
     rs.prefill_packed(a, ins[0], ins[1], None, ins[3], cug, outputs=False)
     if what != "start":
         assert torch.equal(torch.isnan(a.ckpt).cpu(), nan_S)
+
+
+@pytest.mark.parametrize("dtype,ydt", [(BF16, BF16), (BF16, F32), (F32, F32)])
+def test_decays_past_the_range_of_whole_numbers(rs, dtype, ydt):  # noqa: F811
+    """dt so large that a chunk's sum of decays passes 2^31 powers of two: such tokens forget what came before them."""
+    H, G, T = 4, 2, 150
+    ls, A, D, S0 = _layer(rs, 1, H, G, dtype, 97)
+    x, B, C, dt = _scan_inputs(_gen(98), T, H, G, dtype)
+    dt[20:24] = 1e9
+    dt[70:90:3] = 2e9
+    dt[100] = 1e4
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    y = rs.prefill_packed(ls, x.cuda(), B.cuda(), C.cuda(), dt.cuda(), cu, y_dtype=ydt)
+    yr, Sr, ym, Sm = ref.scan(S0[0], x, B, C, dt, A, D)
+    _check_scan(y, ls.ckpt[0], yr, Sr, ym, Sm, "large dt")
