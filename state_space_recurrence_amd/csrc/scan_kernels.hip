@@ -230,11 +230,11 @@ __device__ __forceinline__ int lane_again() {
 // builtin, which makes the compiler wait for it before the transposing reads
 // of the other buffer; the kernel waits for it itself (vmcnt) at the end of a
 // chunk.  Nothing is loaded to a register; m0, the LDS base, is set and used
-// here (the compiler sets it anew before each use of its own).
+// here.
 __device__ __forceinline__ void load_to_lds(u4v resource, int off, unsigned lds) {
     asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(resource),
                  "s"(lds)
-                 : "memory");
+                 : "m0", "memory");
 }
 
 __device__ __forceinline__ u4v resource_of(const void *p, int bytes) {   // a wave-uniform address
