@@ -1,5 +1,5 @@
-"""Post-build checks of the gfx950 machine code: wide-store data hazards
-(run by the build) and the kernels' resource metadata (LDS, VGPRs).
+"""Post-build checks of the gfx950 machine code: wide-store data hazards, scalar
+operands of direct loads to LDS (both run by the build) and the kernels' resource metadata (LDS, VGPRs).
 
 A vector-memory store of more than 64 bits of data (dwordx3 / dwordx4) reads
 its data VGPRs after it issues, so a VALU instruction may overwrite those
@@ -14,6 +14,12 @@ disassembles the device code of every object file and fails if a VALU
 instruction writes a data VGPR of a >64-bit store within two wait states of
 it, whatever the store's offset operands.
 
+A vector-memory instruction may read an SGPR that a VALU instruction wrote (a
+readfirstlane, a compare) only after five wait states.  LLVM inserts them, but
+not into inline assembly, where the packed prefill's direct loads to LDS stand:
+their buffer resources have to come from scalar instructions, or from vector
+ones far enough away.  The check fails for any such load within five wait states.
+
     python -m state_space_recurrence_amd.isa_check [object files...]
 """
 from __future__ import annotations
@@ -27,8 +33,10 @@ import tempfile
 
 LLVM = "/opt/rocm/llvm/bin"
 WAIT_STATES = 2   # required between a >64-bit store and a VALU write of its data
+SCALAR_WAIT_STATES = 5   # required between a VALU write of an SGPR and a vector-memory read of it
 
 _WIDE_STORE = re.compile(r"^(buffer|global|flat|scratch)_store_(dwordx3|dwordx4|b96|b128|format_xyz|format_xyzw)\b")
+_LDS_LOAD = re.compile(r"^buffer_load_\w+ .*\blds$")
 _VREG = re.compile(r"^v\[(\d+):(\d+)\]$|^v(\d+)$")
 
 
@@ -89,6 +97,33 @@ def scan(text: str, wait_states: int = WAIT_STATES):
     return hits
 
 
+def _sregs(text: str) -> set:
+    regs = set()
+    for lo, hi, one in re.findall(r"\bs\[(\d+):(\d+)\]|\bs(\d+)\b", text):
+        regs |= {int(one)} if one else set(range(int(lo), int(hi) + 1))
+    return regs
+
+
+def scan_lds_loads(text: str, wait_states: int = SCALAR_WAIT_STATES):
+    """Direct loads to LDS too soon behind a VALU write of one of their SGPRs:
+    list of (function, line, load, offender)."""
+    insts = list(_instructions(text))
+    hits = []
+    for i, (fn, n, s) in enumerate(insts):
+        if not _LDS_LOAD.match(s):
+            continue
+        read, ws = _sregs(s), 0
+        for _, _, prev in reversed(insts[max(0, i - wait_states):i]):
+            op, _, args = prev.partition(" ")
+            if op.startswith("v_") and _sregs(args.split(",")[0]) & read:
+                hits.append((fn, n, s, prev))
+                break
+            ws += int(args, 0) + 1 if op == "s_nop" else 1
+            if ws >= wait_states:
+                break
+    return hits
+
+
 def _device_object(obj: str, td: str, arch: str) -> str:
     """Extract the gfx950 code object embedded in a hipcc object file."""
     fb, co = os.path.join(td, "fatbin"), os.path.join(td, "dev.co")
@@ -123,13 +158,18 @@ def kernel_resources(obj: str, arch: str = "gfx950") -> dict:
 
 
 def check_objects(objs, arch: str = "gfx950") -> int:
-    """Raise if any object's device code has a wide-store data hazard;
-    returns the number of wide stores seen (for the caller's log)."""
-    bad, seen = [], 0
+    """Raise if any object's device code has a wide-store data hazard or a
+    direct load to LDS too soon behind its operands; returns the number of wide
+    stores seen (for the caller's log)."""
+    bad, early, seen = [], [], 0
     for obj in objs:
         text = disassemble(obj, arch)
         seen += sum(1 for _, _, s in _instructions(text) if _WIDE_STORE.match(s))
         bad += [(os.path.basename(obj),) + h for h in scan(text)]
+        early += [(os.path.basename(obj),) + h for h in scan_lds_loads(text)]
+    if early:
+        lines = "\n".join(f"  {o}: {fn}: {v}  ->  {s}" for o, fn, _, s, v in early[:20])
+        raise RuntimeError(f"{len(early)} direct load(s) to LDS too soon behind a vector write of their SGPRs:\n{lines}")
     if bad:
         lines = "\n".join(f"  {o}: {fn}: {s}  ->  {v}" for o, fn, _, s, v in bad[:20])
         raise RuntimeError(f"{len(bad)} wide-store data hazard(s) in the device code:\n{lines}")
