@@ -27,6 +27,17 @@
 namespace rssm {
 namespace {
 
+// A launch may have 2^32 - 1 threads along an axis: more workgroups than 2^20
+// (2^30 threads) go over two axes.
+constexpr unsigned kGridX = 1u << 20;
+
+inline dim3 grid_of(int64_t blocks) {
+    if (blocks <= kGridX) return dim3((unsigned)blocks);
+    return dim3(kGridX, (unsigned)((blocks + kGridX - 1) / kGridX));
+}
+
+__device__ __forceinline__ int64_t block_index() { return (int64_t)blockIdx.y * kGridX + blockIdx.x; }
+
 // Sum over the THREADS lanes that share a unit (32, 64, or a workgroup).
 template <int THREADS>
 __device__ __forceinline__ float unit_sum(float v, float *lds) {
@@ -63,7 +74,7 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) gated_norm_kern
     __shared__ float lds[16];
     constexpr int kUnits = THREADS < 256 ? 256 / THREADS : 1;
     const int gsize = p.dim / p.groups;
-    const int64_t unit = (int64_t)blockIdx.x * kUnits + (kUnits > 1 ? threadIdx.x / THREADS : 0);
+    const int64_t unit = block_index() * kUnits + (kUnits > 1 ? threadIdx.x / THREADS : 0);
     if (unit >= p.rows * p.groups) return;   // all lanes of the unit
     const int64_t row = unit / p.groups;
     const int c0 = (int)(unit - row * p.groups) * gsize;
@@ -105,7 +116,7 @@ template <typename TX, typename TR, typename TO, int THREADS, int NV, bool FULL>
 __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) add_norm_kernel(AddNormParams p) {
     __shared__ float lds[16];
     constexpr int kUnits = THREADS < 256 ? 256 / THREADS : 1;
-    const int64_t row = (int64_t)blockIdx.x * kUnits + (kUnits > 1 ? threadIdx.x / THREADS : 0);
+    const int64_t row = block_index() * kUnits + (kUnits > 1 ? threadIdx.x / THREADS : 0);
     if (row >= p.rows) return;   // all lanes of the unit
     const int lane = kUnits > 1 ? threadIdx.x % THREADS : threadIdx.x;
     const TX *x = reinterpret_cast<const TX *>(p.x) + row * p.dim;
@@ -178,7 +189,7 @@ hipError_t gated(const GatedNormParams &p, hipStream_t s) {
     return by_size(p.dim / p.groups, [&](auto th, auto nv, auto full) {
         constexpr int TH = decltype(th)::value, NV = decltype(nv)::value;
         const int64_t units = p.rows * p.groups;
-        const dim3 grid((unsigned)((units + kUnitsOf<TH> - 1) / kUnitsOf<TH>)), block(kThreadsOf<TH>);
+        const dim3 grid = grid_of((units + kUnitsOf<TH> - 1) / kUnitsOf<TH>), block(kThreadsOf<TH>);
         hipLaunchKernelGGL((gated_norm_kernel<TY, TZ, TO, TH, NV, decltype(full)::value>), grid, block, 0, s, p);
     });
 }
@@ -187,7 +198,7 @@ template <typename TX, typename TR, typename TO>
 hipError_t added(const AddNormParams &p, hipStream_t s) {
     return by_size(p.dim, [&](auto th, auto nv, auto full) {
         constexpr int TH = decltype(th)::value, NV = decltype(nv)::value;
-        const dim3 grid((unsigned)((p.rows + kUnitsOf<TH> - 1) / kUnitsOf<TH>)), block(kThreadsOf<TH>);
+        const dim3 grid = grid_of((p.rows + kUnitsOf<TH> - 1) / kUnitsOf<TH>), block(kThreadsOf<TH>);
         hipLaunchKernelGGL((add_norm_kernel<TX, TR, TO, TH, NV, decltype(full)::value>), grid, block, 0, s, p);
     });
 }
