@@ -101,7 +101,7 @@ typedef enum rssm_status {
     RSSM_OK = 0,
     RSSM_E_ARG = -1,          /* null pointer, bad size, inconsistent descriptor */
     RSSM_E_UNSUPPORTED = -2,  /* shape / dtype combination not built */
-    RSSM_E_CAPACITY = -3,     /* T > max_draft or Lcap too large */
+    RSSM_E_CAPACITY = -3,     /* T > max_draft, Lcap too large, or more work than one launch holds */
     RSSM_E_HIP = -4,          /* a HIP runtime call failed */
     RSSM_E_DEVICE = -5        /* device-side range error recorded (sticky) */
 } rssm_status;

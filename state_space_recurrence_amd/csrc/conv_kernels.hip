@@ -25,8 +25,8 @@
 namespace rssm {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kVec = 8;
+constexpr int kThreads = kConvThreads;
+constexpr int kVec = kConvVec;
 
 template <typename T>
 __device__ __forceinline__ float dt_of(const ConvParams &p, int64_t token, int h) {
@@ -327,7 +327,7 @@ void launch_tokens(const ConvParams &p, bool advance, hipStream_t s) {
 
 hipError_t launch_conv_tokens(const ConvParams &p0, bool in_bf16, int width, bool advance, hipStream_t s) {
     ConvParams p = p0;
-    p.nblk = (p.Cc / kVec + kThreads - 1) / kThreads;
+    p.nblk = (int)conv_channel_blocks(p.Cc);
     if (in_bf16) {
         RSSM_BY_WIDTH(launch_tokens, uint16_t, (p, advance, s))
     } else {
@@ -338,12 +338,8 @@ hipError_t launch_conv_tokens(const ConvParams &p0, bool in_bf16, int width, boo
 
 hipError_t launch_conv_packed(const ConvParams &p0, bool in_bf16, int width, hipStream_t s) {
     ConvParams p = p0;
-    p.nblk = (p.Cc / kVec + kThreads - 1) / kThreads;
-    // 32 tokens a workgroup read 3 of their neighbour's again; when that leaves
-    // compute units without work, fewer tokens do (down to 4, more than the
-    // W - 1 that HistoryTiles asks for).
-    p.tile = 32;
-    while (p.tile > 4 && (p.total + p.tile - 1) / p.tile * p.nblk < 512) p.tile >>= 1;
+    p.nblk = (int)conv_channel_blocks(p.Cc);
+    p.tile = conv_tile(p.total, p.nblk);
     const dim3 grid((unsigned)((p.total + p.tile - 1) / p.tile * p.nblk)), block(kThreads);
 #define RSSM_PACKED(T, W) hipLaunchKernelGGL((conv_packed_kernel<T, W>), grid, block, 0, s, p)
     switch (width * 2 + (in_bf16 ? 1 : 0)) {

@@ -54,6 +54,22 @@ struct HistoryTiles {
     }
 };
 
+// Workgroups across the channels of a row, and tokens of a packed prompt per
+// workgroup: 32 tokens read 3 of their neighbour's again; when that leaves
+// compute units without work, fewer tokens do (down to 4, more than the W - 1
+// that HistoryTiles asks for).
+constexpr int kConvThreads = 256, kConvVec = 8;
+
+inline int64_t conv_channel_blocks(int64_t channels) {
+    return (channels / kConvVec + kConvThreads - 1) / kConvThreads;
+}
+
+inline int conv_tile(int64_t total, int64_t nblk) {
+    int tile = 32;
+    while (tile > 4 && (total + tile - 1) / tile * nblk < 512) tile >>= 1;
+    return tile;
+}
+
 hipError_t launch_conv_tokens(const ConvParams &p, bool in_bf16, int width, bool advance, hipStream_t s);
 hipError_t launch_conv_packed(const ConvParams &p, bool in_bf16, int width, hipStream_t s);
 hipError_t launch_conv_accept(const ConvParams &p, hipStream_t s);

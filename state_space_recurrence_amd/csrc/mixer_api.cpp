@@ -19,6 +19,13 @@ namespace {
 constexpr int kMinWidth = 2, kMaxWidth = 4, kMaxDraft = 8;
 constexpr int kMaxUnit = 16384;   // elements of a norm's group or row
 
+// A launch holds fewer than 2^32 threads along an axis (one that asks for more
+// runs a part of them without an error).
+int check_threads(const char *what, int64_t threads) {
+    if (threads < (int64_t)1 << 32) return RSSM_OK;
+    return fail(RSSM_E_CAPACITY, "%s: %lld threads are more than a launch holds", what, (long long)threads);
+}
+
 int conv_slots(const rssm_conv_desc *d) { return d->n_slots > 0 ? d->n_slots : d->batch; }
 
 int64_t conv_channels(const rssm_conv_desc *d) {
@@ -115,6 +122,7 @@ int conv_tokens(const rssm_conv_desc *desc, const rssm_conv_state *st, int32_t T
     if (desc->batch == 0) return RSSM_OK;
     RSSM_TRY(check_conv_state(desc, st));
     RSSM_TRY(check_conv_io(desc, io));
+    RSSM_TRY(check_threads("conv", desc->batch * rssm::conv_channel_blocks(conv_channels(desc)) * rssm::kConvThreads));
     rssm::ConvParams p = conv_params(desc, st);
     set_conv_io(p, io);
     p.T = T;
@@ -185,6 +193,8 @@ int replayssm_conv_prefill(const rssm_conv_desc *desc, const rssm_conv_state *st
     RSSM_TRY(check_conv_state(desc, st));
     if (!cu_seqlens) return fail(RSSM_E_ARG, "conv prefill: cu_seqlens is NULL");
     RSSM_TRY(check_conv_io(desc, io));
+    const int64_t nblk = rssm::conv_channel_blocks(conv_channels(desc)), tile = rssm::conv_tile(total, nblk);
+    RSSM_TRY(check_threads("conv prefill", (total + tile - 1) / tile * nblk * rssm::kConvThreads));
     rssm::ConvParams p = conv_params(desc, st);
     set_conv_io(p, io);
     p.cu = cu_seqlens;
