@@ -205,12 +205,6 @@ __global__ void __launch_bounds__(kThreads) conv_packed_kernel(ConvParams p) {
     const int t1 = (int64_t)t0 + p.tile < p.total ? t0 + p.tile : (int)p.total;
     const TIn *u = reinterpret_cast<const TIn *>(p.u) + ch;
 
-    for (int64_t i = (int64_t)t0 * p.H + tid; i < (int64_t)t1 * p.H; i += p.nblk * kThreads) {
-        const int64_t t = i / p.H;
-        const int h = (int)(i - t * p.H);
-        V::put(reinterpret_cast<TIn *>(p.dt) + i, dt_of<TIn>(p, t, h));
-    }
-
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i <= p.rows; i += kThreads)
             if (p.cu[i] < 0 || p.cu[i] > p.total || (i && p.cu[i] < p.cu[i - 1])) atomicOr(p.err, kErrSeq);
@@ -218,6 +212,7 @@ __global__ void __launch_bounds__(kThreads) conv_packed_kernel(ConvParams p) {
     const int s0 = find_sequence(p.cu, p.rows, t0);
     int s = s0;
     if (s < p.rows) {
+        unsigned live = 0;   // of the tile's tokens (32 at most), those of a sequence with a slot
         Taps<TIn, W> taps;
         f8v win[W];
         if (mine) taps.load(p, ch);
@@ -257,7 +252,9 @@ __global__ void __launch_bounds__(kThreads) conv_packed_kernel(ConvParams p) {
                     ring = reinterpret_cast<TIn *>(p.ring) + (size_t)(q.ok ? q.b : 0) * p.R * p.Cc + ch;
                     if (mine) history(t);
                 }
-                if (!q.ok || !mine) continue;
+                if (!q.ok) continue;
+                live |= 1u << (t - t0);
+                if (!mine) continue;
                 win[W - 1] = V::widen(in[j]);
                 V::store(out.base + (int64_t)t * out.pitch, taps.apply(win, p.silu));
 #pragma unroll
@@ -268,6 +265,10 @@ __global__ void __launch_bounds__(kThreads) conv_packed_kernel(ConvParams p) {
                     for (int k = q.m; k < W - 1; ++k)
                         V::store_raw(ring + (size_t)wrap(q.head + q.m - 1 - k, p.R) * p.Cc, V::zero());
             }
+        }
+        for (int i = tid; i < (t1 - t0) * p.H; i += p.nblk * kThreads) {
+            const int t = i / p.H, h = i - t * p.H;
+            if (live >> t & 1) V::put(reinterpret_cast<TIn *>(p.dt) + (int64_t)t0 * p.H + i, dt_of<TIn>(p, t0 + t, h));
         }
         // Publish the heads of the sequences whose history this tile read or
         // wrote, the last of their tiles to arrive does.
