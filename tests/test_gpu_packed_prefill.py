@@ -158,3 +158,54 @@ def test_decays_past_the_range_of_whole_numbers(rs, dtype, ydt):  # noqa: F811
     y = rs.prefill_packed(ls, x.cuda(), B.cuda(), C.cuda(), dt.cuda(), cu, y_dtype=ydt)
     yr, Sr, ym, Sm = ref.scan(S0[0], x, B, C, dt, A, D)
     _check_scan(y, ls.ckpt[0], yr, Sr, ym, Sm, "large dt")
+
+
+@pytest.mark.parametrize("H,G,dtype", [(16, 2, BF16), (10, 2, BF16), (4, 1, BF16), (3, 1, BF16), (4, 2, BF16),
+                                       (2, 2, BF16), (6, 2, F32), (2, 2, F32)])
+def test_bf16_outputs_carry_16_bits_before_their_rounding(rs, H, G, dtype):  # noqa: F811
+    """Several groups, several workgroups a group and heads that fill none, sequences whole and in pieces.
+
+    Of the values formed in fp32 (M, the state) two bf16 parts are taken: each part is off by half a step, 2^-8 of
+    what is left, so 2^-16 of the value.  bf16 inputs are exact operands; all sums are fp32, in about 100 roundings of
+    2^-24 of the terms' sizes at most (products of a chunk, its Gram tile, the state over the chunks), less than
+    2^-17.  fp32 inputs are taken in two parts as well, and of a product of two pairs the last one is left out: three
+    times 2^-16 for C B or S C, as much again for M x.  Then one rounding."""
+    lens = [700, 65, 0, 1300, 1]
+    g, n, slots, cu, fresh = _lens_case(lens, 101)
+    ls, A, D, S0 = _layer(rs, n + 2, H, G, dtype, 103)
+    x, B, C, dt = _scan_inputs(g, sum(lens), H, G, dtype)
+    y = rs.prefill_packed(ls, x.cuda(), B.cuda(), C.cuda(), dt.cuda(), cu.cuda(), fresh=fresh.cuda(), y_dtype=BF16,
+                          slots=slots.cuda())
+    rs.check_device_errors(ls)
+    parts = (2 if dtype == BF16 else 7) * 2.0 ** -16
+    for r in range(n):
+        a, e, s = int(cu[r]), int(cu[r + 1]), int(slots[r])
+        if e == a:
+            continue
+        start = torch.zeros_like(S0[s]) if fresh[r] else S0[s]
+        yr, Sr, ym, Sm = ref.scan(start, x[a:e], B[a:e], C[a:e], dt[a:e], A, D)
+        ref.assert_within(y[a:e], yr, ref.U16 * yr.abs() + (1 + ref.U16) * parts * ym + 1e-30, f"row {r} of {e - a} y")
+        _check_scan(torch.zeros(0, H, 64), ls.ckpt[s], yr[:0], Sr, ym[:0], Sm, f"row {r} of {e - a}")
+
+
+@pytest.mark.parametrize("fmt", ["split-bf16", "split-e4m3", "shared-fp4", "low-bf16", "low-e4m3"])
+@pytest.mark.parametrize("dtype,ydt", [(F32, F32), (F32, BF16), (BF16, BF16)])
+def test_low_precision_states_over_types_and_fresh_rows(rs, fmt, dtype, ydt):  # noqa: F811
+    """Each row equals the row's own replayssm_prefill bit for bit (bf16 outputs: its outputs rounded once)."""
+    lens, H, G = [200, 1, 0, 67], 6, 2
+    g, n, slots, cu, fresh = _lens_case(lens, 107)
+    fresh[0], fresh[3] = 0, 1
+    a, *_ = _layer(rs, n + 2, H, G, dtype, 109, fmt)
+    b, *_ = _layer(rs, n + 2, H, G, dtype, 109, fmt)
+    ins = [t.cuda() for t in _scan_inputs(g, sum(lens), H, G, dtype)]
+    y = rs.prefill_packed(a, *ins, cu.cuda(), fresh=fresh.cuda(), y_dtype=ydt, slots=slots.cuda())
+    for r in range(n):
+        lo, hi = int(cu[r]), int(cu[r + 1])
+        if lo == hi:
+            continue
+        yr = rs.prefill(b, *(t[lo:hi][None].contiguous() for t in ins), from_zero=bool(fresh[r]),
+                        slots=slots[r:r + 1].cuda())
+        assert torch.equal(y[lo:hi], yr[0].to(ydt)), r
+    for k, v in b.tensors().items():
+        assert torch.equal(a.tensors()[k], v), k
+    rs.check_device_errors(a)
