@@ -384,10 +384,12 @@ int replayssm_conv_accept(const rssm_conv_desc *desc, const rssm_conv_state *st,
  * Packed prompts: row r holds tokens cu_seqlens[r] .. cu_seqlens[r+1]-1 of the
  * `total` packed tokens (cu_seqlens [batch+1] int32 device, ascending within
  * 0..total; offsets that do not are flagged, and what the call writes is then
- * undefined, work included: clear it with the state before they are used again).  A row starts from its slot's history, or from zeros where
- * fresh[r] != 0 (fresh [batch] int32 device; NULL: from_zero for every row).
+ * undefined, work included: clear it with the state before they are used
+ * again).  A row starts from its slot's history, or from zeros where fresh[r]
+ * != 0 (fresh [batch] int32 device; NULL: from_zero for every row).
  * The last W-1 inputs of history and prompt become the slot's history.  Rows
- * without tokens leave their slot as it is; tokens of no row are skipped.
+ * without tokens leave their slot as it is; outputs of tokens of no row, or of
+ * a padding row, are left as they are.
  */
 int replayssm_conv_prefill(const rssm_conv_desc *desc, const rssm_conv_state *st, int64_t total,
                            const int32_t *cu_seqlens, int32_t from_zero, const int32_t *fresh,

@@ -12,13 +12,15 @@
 // is a smaller advance of `head`: rejected drafts' rows are overwritten
 // later, as in the replay buffer.  R >= W-1 + Tmax keeps the drafts clear of
 // the history, R >= 2(W-1) the last rows of a prompt clear of the history
-// that other workgroups of the call still read.
+// that other workgroups of the call still read; the new head waits for them
+// (HistoryTiles).
 //
 // All of it is streaming: a thread owns eight channels (16 bytes of bf16) and
 // walks down the tokens with the last W-1 inputs in registers, so each input
 // is read once.  Bound by memory: 16384 tokens of 8192 channels in bf16 take
-// 113 us (537 MB, 4.8 TB/s; with cached instead of streaming loads 130 us), a
-// round of 512 x 5 drafts of 10240 channels 32 us (184 MB, 5.7 TB/s).
+// 109 us (544 MB, 5.0 TB/s; with cached instead of streaming loads 15 % more).
+// A round of 512 x 5 drafts of 10240 channels moves 190 MB: 38 us at the copy
+// rate, 32 us where half of its inputs are still in a cache (87 MB read).
 #include "mixer.h"
 #include "mixer_device.h"
 

@@ -34,21 +34,22 @@
 // and a fractional power of two: a difference of two long sums would
 // otherwise lose the bits of a short one.
 //
-// What bounds it.  One sequence of 16384 tokens, 96 heads in 8 groups, bf16:
-// 33 us for the first launch and 195 us for the second while the clock holds
-// (240 us in long runs), where 473 MB would take 96 us at the copy rate.  Of a
-// chunk's 15000 cycles a SIMD's two waves need 6400 for matrix instructions,
-// and each wave 5500 to issue its 1250 vector instructions (most of them split
-// the state and M into parts).  A wave issues one instruction at a time, so
-// what counts is that neither products nor LDS reads are waited for: operands
-// are read a step ahead, and the next step's vector work stands between the
-// products of the last (without both 214 us, with the reads alone 205).  More
-// than two waves a SIMD would need more than the LDS: a chunk is 64 KB, twice.
-// With fp32 outputs a chunk takes 122 products instead of 98, and 20000 cycles.
+// What bounds it.  One sequence of 16384 tokens, 96 heads in 8 groups, bf16,
+// call after call: 42 us for the first launch and 232 us for the second (the
+// median; 35 and 196 us the shortest, before the clock falls), where 479 MB
+// would take 97 us at the copy rate.  Of a chunk's 15000 cycles a SIMD's two
+// waves need 6400 for matrix instructions, and each wave 5500 to issue its 1250
+// vector instructions (most of them split the state and M into parts).  A wave
+// issues one instruction at a time, so what counts is that neither products nor
+// LDS reads are waited for: operands are read a step ahead, and the next step's
+// vector work stands between the products of the last (second launch, shortest:
+// without both 214 us, with the reads alone 205).  More than two waves a SIMD
+// would need more than the LDS: a chunk is 64 KB, twice.  With fp32 outputs a
+// chunk takes 122 products instead of 98, and 20000 cycles.
 //
 // Order.  Whole segments run first, then the sequences' rests by falling
 // length: 23 sequences of 9001 tokens together, 128 heads, fp32 outputs, took
-// 254 us a call so and 283 us in the sequences' own order (237 us now).
+// 254 us a call so and 283 us in the sequences' own order (240 us now).
 //
 // Long sequences.  When sequences x heads do not fill the card, a sequence is
 // cut into segments: a first launch leaves each segment's end state (the first
