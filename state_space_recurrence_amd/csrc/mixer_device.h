@@ -98,8 +98,8 @@ __device__ __forceinline__ void store_part(T *p, f8v v, int left) {
         if (i < left) vec8<T>::put(p + i, v[i]);
 }
 
-// v sigmoid(v): the exponential overflows to infinity for large negative v,
-// whose reciprocal is the exact limit 0.
+// v sigmoid(v).  For v below -87.3 the reciprocal is below the smallest normal
+// number and is flushed: results of less than 1.2e-36 in size become zero.
 __device__ __forceinline__ float silu(float v) { return v * __builtin_amdgcn_rcpf(1.f + __expf(-v)); }
 
 }  // namespace
