@@ -456,6 +456,78 @@ int replayssm_add_norm(int64_t rows, int32_t dim, const void *x, int32_t x_dtype
                        void *residual_out, int32_t res_dtype, const float *weight, const float *post_weight,
                        float scale, float eps, void *out, int32_t out_dtype, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Projections around a mixer, and rows in 8 bits.
+ *
+ * MX rows (OCP Microscaling, MXFP8): codes [rows, dim] E4M3 ("FN"), dense, one
+ * byte each, starting at a multiple of 16 bytes; scales [rows, dim / 32] E8M0,
+ * dense: element e of a row is code[e] 2^(scale[e / 32] - 127).  dim is a
+ * multiple of 32.  What these calls write: the scale is the least power of two
+ * with amax <= 448 scale, amax the largest finite size among the block's 32
+ * elements (byte 0, 2^-127, at least, and for blocks of zeros); codes are
+ * elements / scale rounded to nearest even; elements that are not finite become
+ * NaN codes.  What they read may have any scale and codes (byte 255: NaN).
+ * ------------------------------------------------------------------------ */
+
+/* Rows to MX: x [rows, dim] at x_pitch elements per row, F32 or BF16. */
+int replayssm_quantize_mx(int64_t rows, int32_t dim, const void *x, int32_t x_dtype, int64_t x_pitch, void *codes,
+                          uint8_t *scales, hipStream_t stream);
+
+/* replayssm_gated_norm with its output in MX (dim / groups a multiple of 32);
+ * the output is quantised from its fp32 values. */
+int replayssm_gated_norm_mx(int64_t rows, int32_t dim, int32_t groups, const void *y, int32_t y_dtype, const void *z,
+                            int32_t z_dtype, int64_t z_pitch, const float *weight, float eps, int32_t norm_before_gate,
+                            void *codes, uint8_t *scales, hipStream_t stream);
+
+/* replayssm_add_norm with its output in MX.  Without x (NULL; residual_out and
+ * post_weight NULL too) it is the norm of the residual alone, for a residual
+ * that replayssm_linear has added to. */
+int replayssm_add_norm_mx(int64_t rows, int32_t dim, const void *x, int32_t x_dtype, const void *residual,
+                          void *residual_out, int32_t res_dtype, const float *weight, const float *post_weight,
+                          float scale, float eps, void *codes, uint8_t *scales, hipStream_t stream);
+
+typedef enum rssm_activation {
+    RSSM_ACT_NONE = 0,
+    RSSM_ACT_SILU = 1,        /* v sigmoid(v) */
+    RSSM_ACT_GELU = 2,        /* v Phi(v), Phi the normal distribution (1.5e-7 |v| off at most) */
+    RSSM_ACT_RELU2 = 3        /* max(v, 0)^2 */
+} rssm_activation;
+
+/* Descriptor of a product (host struct). */
+typedef struct rssm_linear_desc {
+    int64_t rows;
+    int32_t n_in, n_out;      /* 1..2^20 */
+    int32_t in_dtype;         /* x and weight: BF16, or FP8_E4M3 (MX rows) */
+    int32_t out_dtype;        /* F32, BF16, or FP8_E4M3 (MX rows; n_out a multiple of 32) */
+    int32_t res_dtype;        /* F32, BF16, or NONE */
+    int32_t activation;       /* rssm_activation */
+    float scale;
+} rssm_linear_desc;
+
+/* Device buffers of a product (host struct of device pointers). */
+typedef struct rssm_linear_io {
+    const void *x;            /* [rows, n_in] */
+    int64_t x_pitch;          /* elements between rows, n_in .. 2^22; n_in for MX rows */
+    const uint8_t *x_scales;  /* MX rows: their scales */
+    const void *weight;       /* [n_out, n_in] dense */
+    const uint8_t *weight_scales;
+    const float *bias;        /* [n_out] or NULL */
+    const void *residual;     /* [rows, n_out] dense, NULL with res_dtype NONE; may be out where the types agree */
+    void *out;                /* [rows, n_out] dense */
+    uint8_t *out_scales;      /* MX outputs */
+} rssm_linear_io;
+
+/*
+ * Matrix product with its epilogue:
+ *     out = residual + scale act(x weight^T + bias)
+ * in fp32 from the products of the operands' values (MX: the values that codes
+ * and scales stand for), rounded or quantised once.  The order of a sum depends
+ * on the sizes, not on the row: rows of one call with equal inputs get equal
+ * outputs.  bf16 rows of 16-byte aligned address and pitch and of n_in a
+ * multiple of 64, and MX rows of n_in a multiple of 128, take the fast kernels.
+ */
+int replayssm_linear(const rssm_linear_desc *desc, const rssm_linear_io *io, hipStream_t stream);
+
 /* Buffer capacity Lcap = L + Tmax - 1 in entries (0 for an invalid desc). */
 size_t replayssm_buffer_capacity(const rssm_desc *desc);
 

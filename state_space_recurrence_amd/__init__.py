@@ -23,6 +23,7 @@ __all__ = [
     "step", "verify", "accept", "accept_deferred", "commit", "prefill", "load_checkpoint", "recurrent_step",
     "recurrent_verify", "recurrent_accept", "buffer_capacity", "check_device_errors",
     "ConvState", "conv_step", "conv_verify", "conv_accept", "conv_prefill", "prefill_packed", "gated_norm", "add_norm",
+    "linear", "quantize_mx", "gated_norm_mx", "add_norm_mx",
 ]
 
 F32, BF16, FP8_E4M3, FP4_E2M1, NONE = 0, 1, 2, 3, 4
@@ -422,3 +423,4 @@ def recurrent_accept(pool_slots: int, sel, n_keep, T: int, *, heads: int = 1, gr
 
 from .mixer import (ConvState, add_norm, conv_accept, conv_prefill, conv_step, conv_verify,  # noqa: E402
                     gated_norm, prefill_packed)
+from .projection import add_norm_mx, gated_norm_mx, linear, quantize_mx  # noqa: E402

@@ -84,6 +84,7 @@ struct GatedNormParams {
     int dim, groups;
     float eps;
     int before;             // norm before the gate
+    uint8_t *out_scales;    // [rows, dim / 32], MX outputs
 };
 
 struct AddNormParams {
@@ -96,9 +97,22 @@ struct AddNormParams {
     int64_t rows;
     int dim;
     float scale, eps;
+    uint8_t *out_scales;    // [rows, dim / 32], MX outputs
+};
+
+struct QuantizeParams {
+    const void *x;          // [rows, dim], x_pitch elements between rows
+    uint8_t *out;           // [rows, dim] codes, dense
+    uint8_t *out_scales;    // [rows, dim / 32]
+    int64_t x_pitch;
+    int64_t rows;
+    int dim;
 };
 
 hipError_t launch_gated_norm(const GatedNormParams &p, bool y_bf16, bool z_bf16, bool out_bf16, hipStream_t s);
 hipError_t launch_add_norm(const AddNormParams &p, bool x_bf16, bool res_bf16, bool out_bf16, hipStream_t s);
+hipError_t launch_gated_norm_mx(const GatedNormParams &p, bool y_bf16, bool z_bf16, hipStream_t s);
+hipError_t launch_add_norm_mx(const AddNormParams &p, bool x_bf16, bool res_bf16, hipStream_t s);
+hipError_t launch_quantize(const QuantizeParams &p, bool x_bf16, hipStream_t s);
 
 }  // namespace rssm
