@@ -51,104 +51,62 @@ __device__ __forceinline__ float activate(int act, float v) {
     return v;
 }
 
-// Four consecutive outputs n .. n + 3 of row m from their sums; `left` of them
-// are inside the row (whole: left >= 4).
-__device__ __forceinline__ f4v outputs4(const LinearParams &p, int64_t m, int n, f4v v) {
-    const int left = p.n_out - n;
-    if (p.bias) {
-        if (left >= 4) v += *reinterpret_cast<const f4u *>(p.bias + n);
-        else
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (i < left) v[i] += p.bias[n + i];
+// Eight consecutive outputs n .. n + 7 of row m from their sums, some of them
+// in the row (`left`, 1 or more); four neighbouring lanes hold 32 outputs.
+__device__ __forceinline__ void put8(const LinearParams &p, int64_t m, int n, int left, f8v v, const f8v &bias) {
+    const int64_t at = m * p.n_out + n;
+    f8v r = (f8v)0.f;
+    if (p.res) {
+        if (p.res_bf16) r = load_part<false>(static_cast<const uint16_t *>(p.res) + at, left);
+        else r = load_part<false>(static_cast<const float *>(p.res) + at, left);
     }
+    v += bias;
     if (p.act)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = activate(p.act, v[i]);
-    if (!p.res) return p.scale * v;
-    f4v r = (f4v)0.f;
-    const int64_t at = m * p.n_out + n;
-    if (p.res_bf16) {
-        const uint16_t *s = static_cast<const uint16_t *>(p.res) + at;
-        if (left >= 4) {
-            const u2u b = *reinterpret_cast<const u2u *>(s);
-            r = f4v{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xFFFF0000u), __uint_as_float(b.y << 16),
-                    __uint_as_float(b.y & 0xFFFF0000u)};
-        } else {
+        for (int i = 0; i < 8; ++i) v[i] = activate(p.act, v[i]);
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (i < left) r[i] = vec8<uint16_t>::get(s + i);
-        }
-    } else {
-        const float *s = static_cast<const float *>(p.res) + at;
-        if (left >= 4) r = *reinterpret_cast<const f4u *>(s);
-        else
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (i < left) r[i] = s[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = fmaf(p.scale, v[i], r[i]);
-    return v;
-}
-
-__device__ __forceinline__ void store4(const LinearParams &p, int64_t m, int n, f4v v) {
-    const int left = p.n_out - n;
-    const int64_t at = m * p.n_out + n;
-    if (p.out_type == RSSM_BF16) {
-        uint16_t *o = static_cast<uint16_t *>(p.out) + at;
-        if (left >= 4) {
-            typedef __bf16 b4v __attribute__((ext_vector_type(4)));
-            typedef uint32_t u2v __attribute__((ext_vector_type(2)));
-            *reinterpret_cast<u2u *>(o) = __builtin_bit_cast(u2v, __builtin_convertvector(v, b4v));
-        } else {
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (i < left) vec8<uint16_t>::put(o + i, v[i]);
-        }
-    } else {
-        float *o = static_cast<float *>(p.out) + at;
-        if (left >= 4) *reinterpret_cast<f4u *>(o) = v;
-        else
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (i < left) o[i] = v[i];
-    }
-}
-
-// A wave's 32 x 32 tile of sums: outputs n0 .. n0 + 31 (some of them in the
-// row) of rows m0 .. m0 + 31 (the lane's row may lie behind the last).
-__device__ __forceinline__ void finish(const LinearParams &p, int64_t m0, int n0, const f16v &acc, int lane) {
-    const int64_t m = m0 + (lane & 31);
-    const int n = n0 + 4 * (lane >> 5);
-    const bool mine = m < p.rows;
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(p.scale, v[i], r[i]);
     if (p.out_type == RSSM_FP8_E4M3) {   // n_out is a multiple of 32: the block is whole
-        f4v v[4];
         uint32_t a = 0;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            v[g] = (f4v)0.f;
-            if (mine) v[g] = outputs4(p, m, n + 8 * g, f4v{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]});
-#pragma unroll
-            for (int i = 0; i < 4; ++i) a = max(a, mx_size(v[g][i]));
-        }
-        a = max(a, (uint32_t)__shfl_xor((int)a, 32));
+        for (int i = 0; i < 8; ++i) a = max(a, mx_size(v[i]));
+        a = quad_max(a);
         const uint32_t s = mx_scale(a);
         const float inv = mx_inverse(s);
-        if (!mine) return;
-        uint8_t *o = static_cast<uint8_t *>(p.out) + m * p.n_out + n;
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + at) =
+            make_uint2(mx_codes(v[0], v[1], v[2], v[3], inv), mx_codes(v[4], v[5], v[6], v[7], inv));
+        if ((threadIdx.x & 3) == 0) p.out_scales[at / kMxBlock] = (uint8_t)s;
+    } else if (p.out_type == RSSM_BF16) {
+        store_part<false>(static_cast<uint16_t *>(p.out) + at, v, left);
+    } else {
+        store_part<false>(static_cast<float *>(p.out) + at, v, left);
+    }
+}
+
+// A wave's sums of 32 TN outputs (from n0, some of them in the row) x 32 rows
+// (from m0, some of them there), through 4 TN KB of LDS of its own so that a row
+// is stored (and its residual loaded) in one piece.  16 bytes c of row r lie at
+// place c ^ (r & 7).
+template <int TN>
+__device__ __forceinline__ void finish(const LinearParams &p, int64_t m0, int n0, const f16v (&acc)[TN], char *lds, int lane) {
+    constexpr int kPitch = 128 * TN, kAcross = 4 * TN;   // bytes and lanes of a row
+    const int r = lane & 31, h = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<uint32_t *>(o + 8 * g) = mx_codes(v[g][0], v[g][1], v[g][2], v[g][3], inv);
-        if (lane < 32) p.out_scales[m * (p.n_out / kMxBlock) + n0 / kMxBlock] = (uint8_t)s;
-        return;
+            *reinterpret_cast<f4v *>(lds + r * kPitch + (((8 * i + 2 * g + h) ^ (r & 7)) << 4)) =
+                f4v{acc[i][4 * g], acc[i][4 * g + 1], acc[i][4 * g + 2], acc[i][4 * g + 3]};
+    const int c = lane % kAcross, n = n0 + 8 * c, left = p.n_out - n;
+    if (left <= 0) return;   // (all four lanes of a block)
+    f8v bias = (f8v)0.f;
+    if (p.bias) bias = load_part<false>(p.bias + n, left);
+    for (int row = lane / kAcross; row < 32; row += 64 / kAcross) {
+        if (m0 + row >= p.rows) break;
+        const f4v a = *reinterpret_cast<const f4v *>(lds + row * kPitch + (((2 * c) ^ (row & 7)) << 4));
+        const f4v b = *reinterpret_cast<const f4v *>(lds + row * kPitch + (((2 * c + 1) ^ (row & 7)) << 4));
+        put8(p, m0 + row, n, left, f8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, bias);
     }
-    if (!mine) return;
-#pragma unroll
-    for (int g = 0; g < 4; ++g)
-        if (n + 8 * g < p.n_out)
-            store4(p, m, n + 8 * g,
-                   outputs4(p, m, n + 8 * g, f4v{acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]}));
 }
 
 // ---------------------------------------------------------------- products --
@@ -170,32 +128,64 @@ __device__ __forceinline__ b8v widen_codes(const u4v &c, int half, uint32_t scal
     return b8v{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 
-template <bool MX>
-__device__ __forceinline__ void multiply(f16v &acc, const operand &w, const operand &x) {
+// How operands are multiplied.
+enum Product {
+    BF16,       // bf16 rows
+    MX_EXACT,   // MX rows, widened to bf16: products and sums as for bf16 rows
+    MX_FAST     // MX rows, scaled 8-bit products at twice the rate
+};
+
+// One step of a wave's TM x TN tiles of 32 x 32.
+template <Product PR, int TM, int TN>
+__device__ __forceinline__ void multiply(f16v (&acc)[TM][TN], const operand (&w)[TN], const operand (&x)[TM]) {
+    if constexpr (PR == MX_FAST) {   // (the lane's scales were moved to bytes 0 and 2)
+        const auto pair = [](const operand &o, int s) {
+            return i8v{(int)o.c[s].x,     (int)o.c[s].y,     (int)o.c[s].z,     (int)o.c[s].w,
+                       (int)o.c[s + 1].x, (int)o.c[s + 1].y, (int)o.c[s + 1].z, (int)o.c[s + 1].w};
+        };
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        if constexpr (MX) {
+        for (int i = 0; i < TN; ++i)
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
-                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen_codes(w.c[s], half, (w.scales >> (8 * s)) & 0xFFu),
-                                                              widen_codes(x.c[s], half, (x.scales >> (8 * s)) & 0xFFu),
-                                                              acc, 0, 0, 0);
-        } else {
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8v, w.c[s]), __builtin_bit_cast(b8v, x.c[s]),
-                                                          acc, 0, 0, 0);
+            for (int j = 0; j < TM; ++j)
+                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pair(w[i], 0), pair(x[j], 0), acc[j][i], 0, 0, 0,
+                                                                            (int)w[i].scales, 0, (int)x[j].scales);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+                acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pair(w[i], 2), pair(x[j], 2), acc[j][i], 0, 0, 2,
+                                                                            (int)w[i].scales, 2, (int)x[j].scales);
+        return;
+    }
+    constexpr int kParts = PR == BF16 ? 4 : 8;   // products of 16 elements of K each
+#pragma unroll
+    for (int s = 0; s < kParts; ++s) {
+        const auto part = [s](const operand &o) {
+            if constexpr (PR == BF16) return __builtin_bit_cast(b8v, o.c[s]);
+            else return widen_codes(o.c[s >> 1], s & 1, (o.scales >> (8 * (s >> 1))) & 0xFFu);
+        };
+        b8v b[TM];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) b[j] = part(x[j]);
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+            const b8v a = part(w[i]);
+#pragma unroll
+            for (int j = 0; j < TM; ++j) acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[j], acc[j][i], 0, 0, 0);
         }
     }
 }
 
-// Rows 0..31 of `tile` (LDS, at a multiple of 8 rows) as an operand.
-template <bool MX>
-__device__ __forceinline__ operand read_operand(const char *tile, const uint32_t *scales, int lane) {
+// Rows 0..31 of `tile` (LDS, at a multiple of 16 rows) as an operand, with the
+// step's scales of a row every `at_row` bytes.
+template <Product PR>
+__device__ __forceinline__ operand read_operand(const char *tile, const char *scales, int at_row, int lane) {
     operand o;
     const int r = lane & 31, h = lane >> 5;
     const char *p = tile + r * kStep;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) o.c[s] = *reinterpret_cast<const u4v *>(p + (((2 * s + h) ^ (r & 7)) << 4));
-    o.scales = MX ? scales[r] : 0;
+    for (int s = 0; s < 4; ++s) o.c[s] = *reinterpret_cast<const u4v *>(p + (((2 * s + h) ^ ((r >> 1) & 7)) << 4));
+    o.scales = PR == BF16 ? 0 : *reinterpret_cast<const uint32_t *>(scales + r * at_row) >> (PR == MX_FAST ? 8 * h : 0);
     return o;
 }
 
@@ -256,12 +246,12 @@ __global__ void __launch_bounds__(256) linear_any_kernel(LinearParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = (threadIdx.x >> 3) + 32 * i;
-            *reinterpret_cast<u4v *>(&tile[buf][r * kStep + (((threadIdx.x & 7) ^ (r & 7)) << 4)]) = c[i];
+            *reinterpret_cast<u4v *>(&tile[buf][r * kStep + (((threadIdx.x & 7) ^ ((r >> 1) & 7)) << 4)]) = c[i];
         }
         if (MX && threadIdx.x < 2 * B) scales[buf][threadIdx.x] = sc;
     };
 
-    f16v acc = (f16v)0.f;
+    f16v acc[1][1] = {{(f16v)0.f}};
     const int wn = 32 * (wave & 1), wm = B + 32 * (wave >> 1);
     const int steps = (p.k_bytes + kStep - 1) / kStep;
     load(0);
@@ -269,20 +259,533 @@ __global__ void __launch_bounds__(256) linear_any_kernel(LinearParams p) {
     for (int k = 0; k < steps; ++k) {
         if (k + 1 < steps) load(k + 1);
         __syncthreads();
-        const operand w = read_operand<MX>(&tile[k & 1][wn * kStep], &scales[k & 1][wn], lane);
-        const operand x = read_operand<MX>(&tile[k & 1][wm * kStep], &scales[k & 1][wm], lane);
-        multiply<MX>(acc, w, x);
+        const operand w[1] = {read_operand<MX ? MX_EXACT : BF16>(&tile[k & 1][wn * kStep], reinterpret_cast<const char *>(&scales[k & 1][wn]), 4, lane)};
+        const operand x[1] = {read_operand<MX ? MX_EXACT : BF16>(&tile[k & 1][wm * kStep], reinterpret_cast<const char *>(&scales[k & 1][wm]), 4, lane)};
+        multiply<MX ? MX_EXACT : BF16>(acc, w, x);
         if (k + 1 < steps) put((k + 1) & 1);
     }
-    if (n0 + wn < p.n_out) finish(p, m0 + wm - B, n0 + wn, acc, lane);
+    __syncthreads();   // the last step was read
+    finish<1>(p, m0 + wm - B, n0 + wn, acc[0], tile[0] + 4096 * wave, lane);
 }
+
+// ------------------------------------------------------------ direct loads --
+
+// 16 (or 4) bytes a lane from buffer + off + at to the wave's 1024 (256) bytes
+// of LDS at `lds`.  Written out, since the compiler would wait for every such
+// load before any read of LDS.  Nothing is loaded to a register; m0, the LDS
+// base, is set and used in one block.  The buffers are made at the start of a
+// kernel, far enough ahead for their scalar registers.
+__device__ __forceinline__ void load_to_lds16(u4v buffer, int off, int at, unsigned lds) {
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(off),
+                 "s"(buffer), "s"(at), "s"(lds)
+                 : "m0", "memory");
+}
+__device__ __forceinline__ void load_to_lds4(u4v buffer, int off, int at, unsigned lds) {
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(off), "s"(buffer),
+                 "s"(at), "s"(lds)
+                 : "m0", "memory");
+}
+
+// A buffer resource over `bytes` bytes at a wave-uniform address.
+__device__ __forceinline__ u4v resource(const void *p, int bytes) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    return u4v{(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u),
+               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32) & 0xFFFFu),
+               (uint32_t)__builtin_amdgcn_readfirstlane(bytes), (uint32_t)kBufferRsrcWord3};
+}
+
+// The wave's LDS reads and all but LEFT of its loads are done, and every wave
+// of the workgroup got here.
+template <int LEFT>
+__device__ __forceinline__ void arrive() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LEFT) : "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void arrive_loading() {   // the same, with loads in flight
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ __forceinline__ unsigned lds_offset(const void *p) {
+    typedef __attribute__((address_space(3))) const void lds_void;
+    return __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)(lds_void *)p);
+}
+
+// Which tile a workgroup takes.  Workgroups go to the 8 XCDs in turn, so each
+// XCD is given one stretch of the order (its L2 then holds what its tiles
+// share), and the order goes through GROUP rows of tiles at a time.
+template <int GROUP>
+__device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_n, unsigned tiles_m, unsigned &tn, unsigned &tm) {
+    const unsigned tiles = tiles_n * tiles_m, each = tiles / 8, more = tiles % 8, x = id % 8;
+    const unsigned t = x * each + min(x, more) + id / 8;
+    const unsigned band = t / (GROUP * tiles_n), in = t - band * GROUP * tiles_n;
+    const unsigned high = min((unsigned)GROUP, tiles_m - band * GROUP);
+    tn = in / high;
+    tm = band * GROUP + in - tn * high;
+}
+
+// One side's rows of a tile, on their way to LDS: ROWS rows by WAVES waves, a
+// load of eight rows each.  Rows behind the last are the last again.
+template <int ROWS, int WAVES>
+struct RowLoads {
+    static constexpr int kLoads = ROWS / 8 / WAVES;
+    u4v rows;
+    int off[kLoads];
+    __device__ __forceinline__ RowLoads(const void *p, int64_t pitch, int64_t first, int64_t count, int k_bytes, int wave,
+                                        int lane) {
+        const int last = (int)min((int64_t)ROWS, count - first) - 1;
+        rows = resource(static_cast<const char *>(p) + first * pitch, (int)(last * pitch) + k_bytes);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = 8 * (wave + i * WAVES) + lane / 8;
+            off[i] = min(r, last) * (int)pitch + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+        }
+    }
+    __device__ __forceinline__ void issue(int k, unsigned lds, int wave) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) load_to_lds16(rows, off[i], k * kStep, lds + 1024 * (wave + i * WAVES));
+    }
+};
+
+// ------------------------------------------------------------- wide tiles --
+
+// 256 outputs x 256 rows, eight waves of 128 x 64, four half steps (64 bytes of
+// K) in LDS.  The two waves of a SIMD alternate: while one multiplies the half
+// step that it holds in registers, the other reads its next operands, so the
+// matrix cores always have one of them to work for.  Chunk c of row r of a half
+// step lies at place c ^ (r >> 2 & 3) of its 64 bytes.
+template <Product PR>
+__global__ void __launch_bounds__(512) linear_wide_kernel(LinearParams p) {
+    constexpr int B = 256, kHalf = kStep / 2, kSide = B * kHalf, kStages = 4;
+    constexpr int kLoads = 4;   // of a wave and half step
+    constexpr int kGroup = 8;   // half steps whose scales (16 bytes a row) are loaded together
+    __shared__ __attribute__((aligned(1024))) char tile[kStages][2 * kSide];
+    __shared__ __attribute__((aligned(1024))) char scales[2][PR == BF16 ? 16 : 2 * B * 16];
+    unsigned tn, tm;
+    tile_of<8>(blockIdx.x, (p.n_out + B - 1) / B, (unsigned)((p.rows + B - 1) / B), tn, tm);
+    const int n0 = tn * B;
+    const int64_t m0 = (int64_t)tm * B;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    // A wave loads rows 16 (wave + 8 i) .. + 15 of both sides; rows behind the last are the last again.
+    const int last_n = min(B, p.n_out - n0) - 1, last_m = (int)min((int64_t)B, p.rows - m0) - 1;
+    const u4v rw = resource(static_cast<const char *>(p.w) + n0 * p.w_pitch, (int)(last_n * p.w_pitch) + p.k_bytes);
+    const u4v rx = resource(static_cast<const char *>(p.x) + m0 * p.x_pitch, (int)(last_m * p.x_pitch) + p.k_bytes);
+    int ow[2], ox[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = 16 * (wave + 8 * i) + lane / 4, c = (lane & 3) ^ ((lane >> 4) & 3);
+        ow[i] = min(r, last_n) * (int)p.w_pitch + 16 * c;
+        ox[i] = min(r, last_m) * (int)p.x_pitch + 16 * c;
+    }
+    u4v rs = (u4v)0u;
+    int os = 0;
+    if constexpr (PR != BF16) {   // waves 0..3 load the scales of w's rows, 4..7 those of x's
+        const int per = p.k_bytes / kMxBlock, last = wave < 4 ? last_n : last_m;
+        rs = resource(wave < 4 ? p.w_scales + (int64_t)n0 * per : p.x_scales + m0 * per, (last + 1) * per);
+        os = min(64 * (wave & 3) + lane, last) * per;
+    }
+    const unsigned lds = lds_offset(tile), lds_sc = lds_offset(scales);
+    const int halves = p.k_bytes / kHalf;
+    // Rows whose scales are whole groups: 16 bytes of a row together.  Others: the groups' steps one after the other.
+    const bool whole = halves % kGroup == 0;
+    const int at_row = whole ? 16 : 4, at_step = whole ? 4 : 8 * B;
+    const auto issue_scales = [&](int g) {
+        const unsigned to = lds_sc + (g & 1) * 32 * B + 64 * at_row * wave;
+        if (whole) {
+            load_to_lds16(rs, os, 16 * min(g, halves / kGroup - 1), to);
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) load_to_lds4(rs, os, 4 * min(4 * g + s, halves / 2 - 1), to + s * at_step);
+        }
+    };
+    // Behind the end the last half step is loaded again, for nobody: a constant number of loads is in flight.
+    const auto issue = [&](int j) {
+        const int at = min(j, halves - 1) * kHalf;
+        const unsigned to = lds + (j & 3) * 2 * kSide + 1024 * wave;
+        load_to_lds16(rw, ow[0], at, to);
+        load_to_lds16(rw, ow[1], at, to + 8192);
+        load_to_lds16(rx, ox[0], at, to + kSide);
+        load_to_lds16(rx, ox[1], at, to + kSide + 8192);
+        if constexpr (PR != BF16)   // (in time for half step j - j % 8 + 8; the waits below count four loads, at most one too few)
+            if ((j & (kGroup - 1)) == 3) issue_scales(j / kGroup + 1);
+    };
+
+    f16v acc[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][i] = (f16v)0.f;
+    u4v w[4][2], x[2][2];
+    uint32_t sw[4], sx[2];
+    const int wn = 128 * (wave >> 2), wm = 64 * (wave & 3);
+    const int r = lane & 31, h = lane >> 5, place = (h ^ ((r >> 2) & 3)) << 4;
+    const auto read = [&](int j) {
+        const char *t = tile[j & 3] + r * kHalf;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                x[i][s] = *reinterpret_cast<const u4v *>(t + kSide + (wm + 32 * i) * kHalf + (place ^ (32 * s)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i][s] = *reinterpret_cast<const u4v *>(t + (wn + 32 * i) * kHalf + (place ^ (32 * s)));
+        }
+        if constexpr (PR != BF16) {   // MX_FAST: the lane's one scale in byte 0; MX_EXACT: of chunks s = 0, 1 in bytes 0, 1
+            const char *sc = scales[(j / kGroup) & 1] + at_step * ((j >> 1) & 3) + r * at_row;
+            const int shift = 16 * (j & 1) + (PR == MX_FAST ? 8 * h : 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sx[i] = *reinterpret_cast<const uint32_t *>(sc + (B + wm + 32 * i) * at_row) >> shift;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sw[i] = *reinterpret_cast<const uint32_t *>(sc + (wn + 32 * i) * at_row) >> shift;
+        }
+    };
+    const auto work = [&] {
+        if constexpr (PR == MX_FAST) {
+            const auto pair = [](const u4v (&c)[2]) {
+                return i8v{(int)c[0].x, (int)c[0].y, (int)c[0].z, (int)c[0].w, (int)c[1].x, (int)c[1].y, (int)c[1].z, (int)c[1].w};
+            };
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(pair(w[i]), pair(x[j]), acc[j][i], 0, 0, 0,
+                                                                                (int)sw[i], 0, (int)sx[j]);
+            return;
+        }
+        constexpr int kParts = PR == BF16 ? 2 : 4;
+#pragma unroll
+        for (int s = 0; s < kParts; ++s) {
+            const auto part = [s](const u4v (&c)[2], uint32_t sc) {
+                if constexpr (PR == BF16) return __builtin_bit_cast(b8v, c[s]);
+                else return widen_codes(c[s >> 1], s & 1, (sc >> (8 * (s >> 1))) & 0xFFu);
+            };
+            b8v b[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) b[j] = part(x[j], PR == BF16 ? 0 : sx[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const b8v a = part(w[i], PR == BF16 ? 0 : sw[i]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[j], acc[j][i], 0, 0, 0);
+            }
+        }
+    };
+
+    // Slot 2j: waves 0..3 read half step j, slot 2j + 1: they multiply it and 4..7
+    // read it, slot 2j + 2: 4..7 multiply it.  A set asks for half step j + 3 when it
+    // has asked LDS for j: j - 1, which it replaces, was read by all before slot 2j.
+    // j + 1 has to be there at the end of slot 2j + 1, with j + 2 and j + 3 still on
+    // their way.
+    if constexpr (PR != BF16) issue_scales(0);
+    issue(0);
+    issue(1);
+    issue(2);
+    arrive<2 * kLoads>();
+    if (wave < 4) {
+        for (int j = 0; j < halves; ++j) {
+            read(j);
+            issue(j + 3);
+            arrive_loading();
+            __builtin_amdgcn_s_setprio(1);
+            work();
+            __builtin_amdgcn_s_setprio(0);
+            arrive<2 * kLoads>();
+        }
+        arrive_loading();
+    } else {
+        arrive_loading();
+        for (int j = 0; j < halves; ++j) {
+            read(j);
+            issue(j + 3);
+            arrive<2 * kLoads>();
+            __builtin_amdgcn_s_setprio(1);
+            work();
+            __builtin_amdgcn_s_setprio(0);
+            arrive_loading();
+        }
+    }
+    arrive<0>();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) finish<4>(p, m0 + wm + 32 * j, n0 + wn, acc[j], tile[0] + 16384 * wave, lane);
+}
+
+// ------------------------------------------------------------ small tiles --
+
+// BN outputs x BM rows by WN x WM waves, STAGES steps in LDS: every wave asks for
+// step k + STAGES - 1 before it multiplies step k.
+template <Product PR, int BN, int BM, int WN, int WM, int STAGES>
+__global__ void __launch_bounds__(64 * WN * WM) linear_tile_kernel(LinearParams p) {
+    constexpr int kWaves = WN * WM, TN = BN / WN / 32, TM = BM / WM / 32, kRows = BN + BM, kStage = kRows * kStep;
+    constexpr int kLoads = kRows / 8 / kWaves, kScaleLoads = PR == BF16 ? 0 : (kRows / 64 + kWaves - 1) / kWaves;
+    constexpr int kScaleFour = PR == BF16 ? 16 : kRows * 16;   // bytes of four steps' scales
+    static_assert(STAGES <= 5, "a four's scales are asked for no later than its first step");
+    static_assert(kRows / 8 % kWaves == 0 && BN % 64 == 0 && BM % 64 == 0, "whole loads");
+    static_assert(STAGES * kStage >= kWaves * TN * 4096, "sums pass through the stages");
+    __shared__ __attribute__((aligned(1024))) char tile[STAGES][kStage];
+    __shared__ __attribute__((aligned(1024))) char scales[2][kScaleFour];
+    unsigned tn, tm;
+    tile_of<8>(blockIdx.x, (p.n_out + BN - 1) / BN, (unsigned)((p.rows + BM - 1) / BM), tn, tm);
+    const int n0 = tn * BN;
+    const int64_t m0 = (int64_t)tm * BM;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const RowLoads<BN, kWaves> lw(p.w, p.w_pitch, n0, p.n_out, p.k_bytes, wave, lane);
+    const RowLoads<BM, kWaves> lx(p.x, p.x_pitch, m0, p.rows, p.k_bytes, wave, lane);
+    const int steps = p.k_bytes / kStep;
+    // Scales come for four steps together where rows have whole fours (see the wide tiles).
+    const bool whole = steps % 4 == 0;
+    const int at_row = whole ? 16 : 4, at_step = whole ? 4 : 4 * kRows;
+    // Few rows: the weights are read once, by tiles side by side, which start 12
+    // steps apart and go round, so that they do not all ask the same channels for
+    // the same part of K (64 rows of 14432 x 4096: 29.6 -> 27.1 us).  Tiles that share
+    // weights stay together (1024 rows of 4096 x 6144: 63 us, apart 70).
+    const bool apart = whole && p.rows <= BM;
+    const int start = apart ? 4 * (3 * tn % (steps / 4)) : 0;
+    u4v sc[kScaleLoads ? kScaleLoads : 1];
+    int soff[kScaleLoads ? kScaleLoads : 1], sto[kScaleLoads ? kScaleLoads : 1];
+    if constexpr (PR != BF16) {   // 64 rows' scales a load: w's, then x's (waves without rows load others' again)
+        const int per = p.k_bytes / kMxBlock;
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; ++i) {
+            const int at = 64 * ((wave + i * kWaves) % (kRows / 64));
+            const bool ofw = at < BN;
+            const int64_t row0 = ofw ? n0 : m0;
+            const int last = (int)min((int64_t)(ofw ? BN : BM), (ofw ? (int64_t)p.n_out : p.rows) - row0) - 1;
+            sc[i] = resource((ofw ? p.w_scales : p.x_scales) + row0 * per, (last + 1) * per);
+            soff[i] = min(at - (ofw ? 0 : BN) + lane, last) * per;
+            sto[i] = at * at_row;
+        }
+    }
+    const unsigned lds = lds_offset(tile), lds_sc = lds_offset(scales);
+    const auto issue_scales = [&](int g) {
+#pragma unroll
+        for (int i = 0; i < kScaleLoads; ++i) {
+            const unsigned to = lds_sc + (g & 1) * kScaleFour + sto[i];
+            if (whole) {
+                const int at = min(g, steps / 4 - 1) + start / 4;
+                load_to_lds16(sc[i], soff[i], 16 * (at >= steps / 4 ? at - steps / 4 : at), to);
+            } else {
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    load_to_lds4(sc[i], soff[i], 4 * min(4 * g + s, steps - 1), to + s * at_step);
+            }
+        }
+    };
+    // Steps behind the last are the last again (a constant number of loads is in flight); nothing reads them.
+    const auto issue = [&](int k, int stage) {
+        int at = min(k, steps - 1) + start;
+        at = at >= steps ? at - steps : at;
+        lw.issue(at, lds + stage * kStage, wave);
+        lx.issue(at, lds + stage * kStage + BN * kStep, wave);
+    };
+    f16v acc[TM][TN];
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+        for (int i = 0; i < TN; ++i) acc[j][i] = (f16v)0.f;
+    const int wn = BN / WN * (wave % WN), wm = BM / WM * (wave / WN);
+    if constexpr (PR != BF16) issue_scales(0);
+#pragma unroll
+    for (int k = 0; k < STAGES - 1; ++k) issue(k, k);
+    int stage = 0, next = STAGES - 1;
+    for (int k = 0; k < steps; ++k) {
+        arrive<(STAGES - 2) * kLoads>();   // (scales in between make it wait for more)
+        if constexpr (PR != BF16)   // into the place of the four before, which all have read
+            if ((k & 3) == 0) issue_scales(k / 4 + 1);
+        issue(k + STAGES - 1, next);
+        operand w[TN], x[TM];
+        const char *t = tile[stage], *s = scales[(k >> 2) & 1] + (k & 3) * at_step;
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+            x[j] = read_operand<PR>(t + (BN + wm + 32 * j) * kStep, s + (BN + wm + 32 * j) * at_row, at_row, lane);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+            w[i] = read_operand<PR>(t + (wn + 32 * i) * kStep, s + (wn + 32 * i) * at_row, at_row, lane);
+        multiply<PR>(acc, w, x);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        next = next + 1 == STAGES ? 0 : next + 1;
+    }
+    arrive<0>();
+#pragma unroll
+    for (int j = 0; j < TM; ++j) finish<TN>(p, m0 + wm + 32 * j, n0 + wn, acc[j], tile[0] + 4096 * TN * wave, lane);
+}
+
+// ---------------------------------------------------------------- few rows --
+
+// 16 NT outputs x 16 MT rows by a workgroup whose waves share K: each takes every
+// WAVES-th step, AHEAD of them at a time, straight from memory to registers, and
+// their sums are added in LDS in the order of the waves.  16 x 16 tiles: lane l
+// holds row l % 16 of an operand, chunks l / 16 and 4 + l / 16 of a step, and
+// those lie in blocks l / 32 and 2 + l / 32.
+template <bool MX, int WAVES, int NT, int MT, int AHEAD>
+__global__ void __launch_bounds__(64 * WAVES) linear_few_kernel(LinearParams p) {
+    __shared__ f4v part[WAVES][MT][NT][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+    unsigned tn, tm;
+    tile_of<8>(blockIdx.x, (p.n_out + 16 * NT - 1) / (16 * NT), (unsigned)((p.rows + 16 * MT - 1) / (16 * MT)), tn, tm);
+    const int n0 = tn * 16 * NT;
+    const int64_t m0 = (int64_t)tm * 16 * MT;
+    const int per = p.k_bytes / kMxBlock;
+    const char *x[MT], *w[NT];
+    const uint8_t *xs[MT], *ws[NT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j) {   // rows behind the last are the last again
+        const int64_t m = min(m0 + 16 * j + r, p.rows - 1);
+        x[j] = static_cast<const char *>(p.x) + m * p.x_pitch + 16 * q;
+        xs[j] = MX ? p.x_scales + m * per : nullptr;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int64_t n = min(n0 + 16 * t + r, p.n_out - 1);
+        w[t] = static_cast<const char *>(p.w) + n * p.w_pitch + 16 * q;
+        ws[t] = MX ? p.w_scales + n * per : nullptr;
+    }
+    f4v acc[MT][NT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[j][t] = (f4v)0.f;
+    struct step {
+        u4v c[2];
+        uint32_t s;
+    };
+    const int steps = p.k_bytes / kStep;
+    const auto load = [&](const char *v, const uint8_t *scales, int k) {   // behind the last step: zeros
+        step o;
+        const bool in = k < steps;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) o.c[i] = in ? *reinterpret_cast<const u4v *>(v + k * kStep + 64 * i) : (u4v)0u;
+        o.s = MX && in ? *reinterpret_cast<const uint32_t *>(scales + 4 * k) : 0;
+        return o;
+    };
+    for (int k = wave; k < steps; k += AHEAD * WAVES) {
+        step a[AHEAD][NT], b[AHEAD][MT];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) a[u][t] = load(w[t], ws[t], k + u * WAVES);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) b[u][j] = load(x[j], xs[j], k + u * WAVES);
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int half = 0; half < (MX ? 2 : 1); ++half) {
+                    const auto part = [&](const step &o) {
+                        if constexpr (MX) return widen_codes(o.c[i], half, (o.s >> (16 * i + 8 * (q >> 1))) & 0xFFu);
+                        else return __builtin_bit_cast(b8v, o.c[i]);
+                    };
+                    b8v xb[MT];
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) xb[j] = part(b[u][j]);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const b8v wa = part(a[u][t]);
+#pragma unroll
+                        for (int j = 0; j < MT; ++j)
+                            acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wa, xb[j], acc[j][t], 0, 0, 0);
+                    }
+                }
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) part[wave][j][t][lane] = acc[j][t];
+    __syncthreads();
+    // Output n0 + 8 c .. of row m0 + row: the sums i of lanes 16 (n % 16 / 4) + row % 16 of tile n / 16.
+    static_assert(32 * NT * MT <= 64 * WAVES, "a thread for every eight outputs");
+    const int c = threadIdx.x % (2 * NT), row = threadIdx.x / (2 * NT), left = p.n_out - n0 - 8 * c;
+    if (row >= 16 * MT || m0 + row >= p.rows || left <= 0) return;
+    f8v v = (f8v)0.f, bias = (f8v)0.f;
+    if (p.bias) bias = load_part<false>(p.bias + n0 + 8 * c, left);
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+        const f4v *t = part[i][row >> 4][c >> 1] + 32 * (c & 1) + (row & 15);
+        const f4v a = t[0], b = t[16];
+        v += f8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    }
+    put8(p, m0 + row, n0 + 8 * c, left, v, bias);
+}
+
+// Kernels by their tiles, and what a call costs in each: a part that every call
+// has and one for each round of 256 tiles (one per compute unit), fitted to calls
+// of 1 to 16384 rows of 256 to 16384 outputs; 1 is what 64 x 64 tiles take for one
+// round.  Small tiles keep all units at work, large ones load less for each
+// product: of 6144 inputs and 4096 outputs in bf16, 64 rows take 45 us in 16 x 16
+// tiles, 26 in 32 x 32, 34 in 64 x 64; 1024 rows 96 in 64 x 64, 63 in 128 x 128, 144
+// in 256 x 256; 8192 rows of 8192 x 8192 1560, 1125 and 862.
+enum Tile { T16, T32x16, T32, T64, T64x128, T128, T256, kTiles };
+struct TileCost {
+    int n, m;
+    float call[3], round[3];   // by Product
+};
+constexpr TileCost kTileCosts[kTiles] = {
+    {16, 16, {.12f, .19f, .19f}, {.24f, .37f, .37f}},   {32, 16, {.14f, .23f, .23f}, {.42f, .56f, .56f}},
+    {32, 32, {.13f, .16f, .16f}, {.48f, .81f, .81f}},   {64, 64, {.55f, .60f, .55f}, {.42f, .55f, .41f}},
+    {64, 128, {.45f, 1e9f, .30f}, {.85f, .0f, .95f}}, {128, 128, {.40f, .0f, .45f}, {1.22f, 2.05f, 1.25f}},
+    {256, 256, {.0f, .0f, .15f}, {3.8f, 6.1f, 3.25f}},
+};
+
+int64_t tiles_of(const LinearParams &p, int n, int m) { return (p.rows + m - 1) / m * ((p.n_out + n - 1) / n); }
+
+Tile best_tile(const LinearParams &p, Product pr) {
+    int best = T64;
+    float least = 3e38f;
+    // (16 outputs are half a block of an MX output)
+    for (int t = p.out_type == RSSM_FP8_E4M3 ? T32x16 : T16; t < kTiles; ++t) {
+        const int64_t rounds = (tiles_of(p, kTileCosts[t].n, kTileCosts[t].m) + 255) / 256;
+        const float cost = kTileCosts[t].call[pr] + kTileCosts[t].round[pr] * rounds;
+        if (cost < least) {
+            least = cost;
+            best = t;
+        }
+    }
+    return (Tile)best;
+}
+
+template <Product PR>
+void launch_direct(const LinearParams &p, hipStream_t s) {
+    constexpr bool MX = PR != BF16;
+    const Tile t = best_tile(p, PR);
+    const dim3 grid((unsigned)tiles_of(p, kTileCosts[t].n, kTileCosts[t].m));
+    switch (t) {
+        case T16: hipLaunchKernelGGL((linear_few_kernel<MX, 8, 1, 1, 2>), grid, dim3(512), 0, s, p); break;
+        case T32x16: hipLaunchKernelGGL((linear_few_kernel<MX, 8, 2, 1, 2>), grid, dim3(512), 0, s, p); break;
+        case T32: hipLaunchKernelGGL((linear_few_kernel<MX, 8, 2, 2, 2>), grid, dim3(512), 0, s, p); break;
+        case T64: hipLaunchKernelGGL((linear_tile_kernel<PR, 64, 64, 2, 2, 4>), grid, dim3(256), 0, s, p); break;
+        case T64x128:   // (MX_EXACT: never the least)
+            if constexpr (PR != MX_EXACT)
+                hipLaunchKernelGGL((linear_tile_kernel<PR, 64, 128, 2, 2, 4>), grid, dim3(256), 0, s, p);
+            break;
+        case T128: hipLaunchKernelGGL((linear_tile_kernel<PR, 128, 128, 2, 4, 4>), grid, dim3(512), 0, s, p); break;
+        default: hipLaunchKernelGGL((linear_wide_kernel<PR>), grid, dim3(512), 0, s, p); break;
+    }
+}
+
+bool multiple(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 }  // namespace
 
 hipError_t launch_linear(const LinearParams &p, bool mx, hipStream_t s) {
-    const int64_t tiles = ((p.rows + 63) / 64) * ((p.n_out + 63) / 64);
-    if (mx) hipLaunchKernelGGL(linear_any_kernel<true>, dim3((unsigned)tiles), dim3(256), 0, s, p);
-    else hipLaunchKernelGGL(linear_any_kernel<false>, dim3((unsigned)tiles), dim3(256), 0, s, p);
+    // Whole steps at aligned addresses are loaded straight to LDS or operands.
+    const bool direct = p.k_bytes % kStep == 0 && p.x_pitch % 16 == 0 && multiple(p.x, 16) && multiple(p.w, 16) &&
+                        (!mx || (multiple(p.x_scales, 4) && multiple(p.w_scales, 4)));
+    if (!direct) {
+        const dim3 grid((unsigned)tiles_of(p, 64, 64));
+        if (mx) hipLaunchKernelGGL(linear_any_kernel<true>, grid, dim3(256), 0, s, p);
+        else hipLaunchKernelGGL(linear_any_kernel<false>, grid, dim3(256), 0, s, p);
+    } else if (!mx) {
+        launch_direct<BF16>(p, s);
+    } else if (p.out_type == RSSM_BF16) {
+        launch_direct<MX_FAST>(p, s);
+    } else {
+        launch_direct<MX_EXACT>(p, s);
+    }
     return hipGetLastError();
 }
 

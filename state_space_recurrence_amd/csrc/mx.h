@@ -13,6 +13,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "device_common.h"
+
 namespace rssm {
 
 constexpr int kMxBlock = 32;   // elements that share a scale
@@ -37,6 +39,12 @@ __device__ __forceinline__ uint32_t mx_scale(uint32_t amax) {
 
 // 1 / scale; a normal number for every byte that mx_scale gives (0..247).
 __device__ __forceinline__ float mx_inverse(uint32_t s) { return __uint_as_float((254u - s) << 23); }
+
+// Largest of four neighbouring lanes' numbers.
+__device__ __forceinline__ uint32_t quad_max(uint32_t m) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadSwap1, 0xF, 0xF, false));
+    return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadRev, 0xF, 0xF, false));
+}
 
 // Four elements to codes, the first in the lowest byte.
 __device__ __forceinline__ uint32_t mx_codes(float a, float b, float c, float d, float inv) {

@@ -77,9 +77,7 @@ __device__ __forceinline__ void store_out(void *out, uint8_t *scales, int64_t ro
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max(m, mx_size(o[i]));
-        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadSwap1, 0xF, 0xF, false));
-        m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, kDppQuadRev, 0xF, 0xF, false));
-        const uint32_t s = mx_scale(m);
+        const uint32_t s = mx_scale(quad_max(m));
         const float inv = mx_inverse(s);
         const uint2 q = make_uint2(mx_codes(o[0], o[1], o[2], o[3], inv), mx_codes(o[4], o[5], o[6], o[7], inv));
         *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(out) + row * dim + c) = q;

@@ -32,13 +32,13 @@ def mx_quantize(v):
 
 def mx_values(pair):
     """The values that codes and scales stand for, in 64 bits."""
-    codes, scales = (t.cpu() for t in pair)
+    codes, scales = pair
     s = torch.exp2(scales.view(torch.uint8).double() - 127)
     return codes.double() * s.repeat_interleave(BLOCK, -1)
 
 
 def mx_pair(v):
-    """(codes, scales) of v on the CPU."""
+    """(codes, scales) of v."""
     q, power = mx_quantize(v)
     return q.to(E4M3), (power + 127).to(torch.uint8).view(E8M0)
 
@@ -46,7 +46,7 @@ def mx_pair(v):
 def assert_mx(pair, want, err, what):
     """An MX result of values that may be off `want` by `err` before they are quantised: scales between those of the
     block's smallest and largest possible amax, elements off by err and half a step of their octave."""
-    got = mx_values(pair)
+    got, want, err = mx_values(pair).cpu(), want.cpu(), err.cpu()
     power = pair[1].cpu().view(torch.uint8).long() - 127
     b, e = (t.reshape(t.shape[0], -1, BLOCK) for t in (want.double(), err.double()))
     lo, hi = mx_power((b.abs() - e).clamp(min=0).amax(-1)), mx_power((b.abs() + e).amax(-1))
@@ -61,13 +61,26 @@ def gelu(v):
     return 0.5 * v * torch.special.erfc(-v / math.sqrt(2))
 
 
-def linear(x, w, bias, act, res, scale):
+def cut_products(x, w):
+    """Error bound of scaled 8-bit products: the matrix units cut a product 13 binary places below the largest of the
+    products that they add at once, some of 16 consecutive ones."""
+    x, w = (torch.nn.functional.pad(t.double().abs(), (0, -t.shape[1] % 16)) for t in (x, w))
+    total = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64, device=x.device)
+    for r in range(0, x.shape[0], 64):
+        for k in range(0, x.shape[1], 16):
+            total[r:r + 64] += (x[r:r + 64, None, k:k + 16] * w[None, :, k:k + 16]).amax(-1)
+    return 16 * 2.0 ** -13 * total
+
+
+def linear(x, w, bias, act, res, scale, cut=False):
     """x [rows,K], w [N,K] (values, any type): outputs in 64 bits and their error bound before the last rounding."""
     x, w = x.double(), w.double()
     v = x @ w.t()
     # K additions into fp32, each off by a step of a partial sum of at most the terms' sum (a half step where the
     # matrix units round to nearest, a whole one where they cut off)
     err = x.shape[1] * 2 * U32 * (x.abs() @ w.abs().t())
+    if cut:
+        err = err + cut_products(x, w)
     if bias is not None:
         v = v + bias.double()
         err = err + U32 * v.abs()

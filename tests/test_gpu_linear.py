@@ -52,14 +52,17 @@ def _operands(x_type, rows, n_out, n_in, seed, zero_row=True):
     return x, w, x, w
 
 
-def _check(rs, x_type, rows, n_out, n_in, out_type, bias, act, res_type, scale, seed=0):
+def _check(rs, x_type, rows, n_out, n_in, out_type, bias, act, res_type, scale, seed=0, at="cpu"):
     x, w, xv, wv = _operands(x_type, rows, n_out, n_in, seed + rows + 7 * n_out + 13 * n_in)
+    xv, wv = xv.to(at), wv.to(at)
     g = _gen(seed + 1)
     b = 0.1 * torch.randn(n_out, generator=g) if bias else None
     r = None if res_type is None else (2 * torch.randn(rows, n_out, generator=g)).to(res_type)
     got = rs.linear(_cuda(x), _cuda(w), _cuda(b), activation=act, residual=_cuda(r), scale=scale,
                     out_dtype=ref.E4M3 if out_type == MX else out_type)
-    want, err = ref.linear(xv, wv, b, act, r, scale)
+    want, err = ref.linear(xv, wv, None if b is None else b.to(at), act, None if r is None else r.to(at), scale,
+                           cut=x_type == MX and out_type == BF16)
+    want, err = want.cpu(), err.cpu()
     if out_type == MX:
         ref.assert_mx(got, want, err, "mx output")
     else:
@@ -212,6 +215,27 @@ def test_epilogue(rs, x_type, rows, n_out, n_in, bias, act, res_type, scale, out
     _check(rs, x_type, rows, n_out, n_in, out_type, bias, act, res_type, scale)
 
 
+# Sizes at which each of the tiles is taken (16 x 16 and 32 x 16 ones by the sizes above): sums of whole fours of steps
+# and others, edges in both directions
+BY_TILE = [(BF16, 20, 4100, 576), (BF16, 32, 4128, 2048), (BF16, 33, 4100, 1024), (BF16, 64, 9000, 1088),
+           (BF16, 65, 9000, 640), (BF16, 128, 9120, 2048), (BF16, 200, 9000, 1088), (BF16, 256, 9120, 2048),
+           (BF16, 2000, 4100, 1088), (BF16, 2048, 4128, 2048), (MX, 20, 4100, 1152), (MX, 33, 4128, 2048),
+           (MX, 64, 9000, 4096), (MX, 65, 9000, 1152), (MX, 128, 9120, 2048), (MX, 200, 9000, 1152),
+           (MX, 256, 9120, 2048), (MX, 2000, 4100, 1152), (MX, 3000, 4128, 2048)]
+
+
+@pytest.mark.parametrize("x_type,rows,n_out,n_in", BY_TILE)
+@pytest.mark.parametrize("out_type,res_type", [(BF16, None), (F32, F32)])
+def test_every_tile(rs, x_type, rows, n_out, n_in, out_type, res_type):
+    """The 64-bit product is taken on the GPU here."""
+    _check(rs, x_type, rows, n_out, n_in, out_type, True, None, res_type, 0.5, at="cuda")
+
+
+@pytest.mark.parametrize("x_type,rows,n_out,n_in", [c for c in BY_TILE if c[2] % 32 == 0])
+def test_every_tile_mx_output(rs, x_type, rows, n_out, n_in):
+    _check(rs, x_type, rows, n_out, n_in, MX, True, "gelu", BF16, 0.5, at="cuda")
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "relu2"])
 def test_activation_values(rs, act):
     """An identity product: the activation over the range of its argument, large ones and zeros among them."""
@@ -224,7 +248,9 @@ def test_activation_values(rs, act):
 
 
 SHAPES_BY_KERNEL = [(BF16, 3, 100, 65), (BF16, 5, 96, 256), (BF16, 40, 160, 256), (BF16, 200, 544, 256), (MX, 5, 96, 256),
-                    (MX, 9, 160, 96), (MX, 40, 160, 256), (MX, 200, 544, 256), (BF16, 600, 1000, 192), (MX, 600, 1000, 256)]
+                    (MX, 9, 160, 96), (MX, 40, 160, 256), (MX, 200, 544, 256), (BF16, 600, 1000, 192), (MX, 600, 1000, 256),
+                    (BF16, 33, 4100, 128), (BF16, 100, 9024, 192), (BF16, 200, 9024, 64), (BF16, 2000, 4128, 64),
+                    (MX, 33, 4100, 256), (MX, 200, 9024, 128), (MX, 3000, 4128, 128)]
 
 
 @pytest.mark.parametrize("x_type,rows,n_out,n_in", SHAPES_BY_KERNEL)
@@ -375,7 +401,7 @@ def test_block_follows_its_formulas(rs):
     g = _gen(8)
     x, res = torch.randn(33, 256, generator=g).to(BF16).cuda(), torch.randn(33, 256, generator=g).cuda()
     got = _block(rs, x, res, p)
-    hw, he = ref.linear(ref.mx_values(p["n"]), ref.mx_values(p["up"]), p["b"].cpu(), "gelu", None, 1.0)
+    hw, he = ref.linear(ref.mx_values(p["n"]), ref.mx_values(p["up"]), p["b"], "gelu", None, 1.0)
     ref.assert_mx(p["h"], hw, he, "hidden rows")
-    want, err = ref.linear(ref.mx_values(p["h"]), ref.mx_values(p["down"]), None, None, p["r"].cpu(), 1.0)
-    mixer_ref.assert_within(got, want, err, "block")
+    want, err = ref.linear(ref.mx_values(p["h"]), ref.mx_values(p["down"]), None, None, p["r"], 1.0)
+    mixer_ref.assert_within(got, want.cpu(), err.cpu(), "block")
