@@ -13,8 +13,8 @@ import ctypes
 
 import torch
 
-from . import BF16, F32, FP8_E4M3, NONE, ReplaySSMError, _check, lib
-from .mixer import _dense, _empty, _float, _pitch, _raw_stream
+from . import BF16, F32, FP8_E4M3, NONE, ReplaySSMError, _check, _need, lib
+from .mixer import _TYPES, _empty, _pitch, _raw_stream
 
 __all__ = ["linear", "quantize_mx", "gated_norm_mx", "add_norm_mx"]
 
@@ -54,23 +54,43 @@ def _lib():
     return L
 
 
-def _device(t: torch.Tensor, *others) -> None:
-    """One device for all tensors of a call, and the one that launches go to."""
-    at = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != at:
-            raise ReplaySSMError(f"all tensors of a call must be on one device, got {at} and {o.get_device()}")
-    if at >= 0 and at != torch.cuda.current_device():
-        raise ReplaySSMError(f"the tensors are on device {at}: make it the current one (torch.cuda.device)")
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _mx(pair, rows: int, dim: int, name: str):
+def _device(t, name: str) -> int:
+    """The device of a call's tensors, which has to be the current one (launches go there).
+    (A token's calls are bound by the host: each tensor is looked at once, in ``_at``.)"""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise ReplaySSMError(f"{name}: expected a device tensor, got "
+                             f"{f'{tuple(t.shape)} {t.dtype} device={t.device}' if isinstance(t, torch.Tensor) else type(t).__name__}")
+    if dev != _current_device():
+        raise ReplaySSMError(f"{name}: is on device {dev}, which is not the current one (torch.cuda.device)")
+    return dev
+
+
+def _at(t: torch.Tensor, shape: tuple, dtype, dev: int, name: str) -> int:
+    """Address of a dense tensor of this shape and type on device ``dev`` (else raise)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, shape, dtype, name)
+    raise ReplaySSMError(f"{name}: is on device {t.get_device()}, the call's other tensors on {dev}")
+
+
+def _type(t, name: str) -> int:
+    ty = _TYPES.get(t.dtype)
+    if ty is None:
+        raise ReplaySSMError(f"{name}: expected fp32 or bf16, got {t.dtype}")
+    return ty
+
+
+def _mx(pair, rows: int, dim: int, dev: int, name: str):
     """Addresses of codes and scales of MX rows (else raise)."""
     if not isinstance(pair, (tuple, list)) or len(pair) != 2:
         raise ReplaySSMError(f"{name}: expected a pair (codes, scales)")
     codes, scales = pair
-    return (_dense(codes, (rows, dim), _E4M3, name + " codes"),
-            _dense(scales, (rows, dim // _BLOCK), _E8M0, name + " scales"))
+    return (_at(codes, (rows, dim), _E4M3, dev, name + " codes"),
+            _at(scales, (rows, dim // _BLOCK), _E8M0, dev, name + " scales"))
 
 
 def _blocks(dim: int, name: str) -> None:
@@ -78,10 +98,8 @@ def _blocks(dim: int, name: str) -> None:
         raise ReplaySSMError(f"{name}: MX rows hold a positive multiple of {_BLOCK} elements, got {dim}")
 
 
-def _mx_out(out, rows: int, dim: int, device, stream):
-    if out is None:
-        out = (_empty((rows, dim), _E4M3, device, stream), _empty((rows, dim // _BLOCK), _E8M0, device, stream))
-    return out, _mx(out, rows, dim, "out")
+def _mx_empty(rows: int, dim: int, device, stream):
+    return _empty((rows, dim), _E4M3, device, stream), _empty((rows, dim // _BLOCK), _E8M0, device, stream)
 
 
 def quantize_mx(x, *, out=None, stream=None):
@@ -91,10 +109,11 @@ def quantize_mx(x, *, out=None, stream=None):
         raise ReplaySSMError(f"x: expected [rows, dim], got {tuple(x.shape)}")
     rows, dim = x.shape
     _blocks(dim, "x")
-    xt = _float(x, "x")
-    pitch = _pitch(x, (rows,), dim, x.dtype, "x")
-    out, (codes, scales) = _mx_out(out, rows, dim, x.device, stream)
-    _device(x, *out)
+    dev, xt = _device(x, "x"), _type(x, "x")
+    pitch = dim if x.is_contiguous() else _pitch(x, (rows,), dim, x.dtype, "x")
+    if out is None:
+        out = _mx_empty(rows, dim, x.device, stream)
+    codes, scales = _mx(out, rows, dim, dev, "out")
     rc = _lib().replayssm_quantize_mx(rows, dim, x.data_ptr(), xt, pitch, codes, scales, _raw_stream(stream, x))
     if rc:
         _check(rc)
@@ -108,14 +127,15 @@ def gated_norm_mx(y, z, weight, *, groups: int = 1, eps: float = 1e-5, norm_befo
         raise ReplaySSMError(f"z: expected [rows, dim], got {tuple(z.shape)}")
     rows, dim = z.shape
     _blocks(dim, "z")
-    yt, zt = _float(y, "y"), _float(z, "z")
-    if y.shape[0] != rows or y.numel() != rows * dim or not y.is_contiguous():
-        raise ReplaySSMError(f"y: expected a dense tensor of {rows} rows of {dim}, got {tuple(y.shape)} "
-                             f"contiguous={y.is_contiguous()}")
+    dev, yt, zt = _device(z, "z"), _type(y, "y"), _type(z, "z")
+    if y.shape[:1] != (rows,) or y.numel() != rows * dim or not y.is_contiguous() or y.get_device() != dev:
+        raise ReplaySSMError(f"y: expected a dense tensor of {rows} rows of {dim} on device {dev}, got {tuple(y.shape)} "
+                             f"contiguous={y.is_contiguous()} device={y.device}")
     pitch = _pitch(z, (rows,), dim, z.dtype, "z")
-    w = _dense(weight, (dim,), torch.float32, "weight")
-    out, (codes, scales) = _mx_out(out, rows, dim, z.device, stream)
-    _device(z, y, weight, *out)
+    w = _at(weight, (dim,), torch.float32, dev, "weight")
+    if out is None:
+        out = _mx_empty(rows, dim, z.device, stream)
+    codes, scales = _mx(out, rows, dim, dev, "out")
     rc = _lib().replayssm_gated_norm_mx(rows, dim, groups, y.data_ptr(), yt, z.data_ptr(), zt, pitch, w, eps,
                                         1 if norm_before_gate else 0, codes, scales, _raw_stream(stream, z))
     if rc:
@@ -132,22 +152,24 @@ def add_norm_mx(x, residual, weight, *, scale: float = 1.0, post_weight=None, ep
         raise ReplaySSMError(f"residual: expected [rows, dim], got {tuple(residual.shape)}")
     rows, dim = shape = residual.shape
     _blocks(dim, "residual")
-    rt = _float(residual, "residual")
-    rp = _dense(residual, shape, residual.dtype, "residual")
-    w = _dense(weight, (dim,), torch.float32, "weight")
-    p = None if post_weight is None else _dense(post_weight, (dim,), torch.float32, "post_weight")
+    dev, ty = _device(residual, "residual"), residual.dtype
+    rt = _type(residual, "residual")
+    rp = _at(residual, shape, ty, dev, "residual")
+    w = _at(weight, (dim,), torch.float32, dev, "weight")
+    p = None if post_weight is None else _at(post_weight, (dim,), torch.float32, dev, "post_weight")
     if x is None:
         if residual_out is not None or post_weight is not None:
             raise ReplaySSMError("x: residual_out and post_weight go with it")
         xp, xt, op = None, F32, None
     else:
-        xt = _float(x, "x")
-        xp = _dense(x, shape, x.dtype, "x")
+        xt = _type(x, "x")
+        xp = _at(x, shape, x.dtype, dev, "x")
         if residual_out is None:
-            residual_out = _empty(shape, residual.dtype, residual.device, stream)
-        op = _dense(residual_out, shape, residual.dtype, "residual_out")
-    out, (codes, scales) = _mx_out(out, rows, dim, residual.device, stream)
-    _device(residual, x, weight, post_weight, residual_out, *out)
+            residual_out = _empty(shape, ty, residual.device, stream)
+        op = _at(residual_out, shape, ty, dev, "residual_out")
+    if out is None:
+        out = _mx_empty(rows, dim, residual.device, stream)
+    codes, scales = _mx(out, rows, dim, dev, "out")
     rc = _lib().replayssm_add_norm_mx(rows, dim, xp, xt, rp, op, rt, w, p, scale, eps, codes, scales,
                                       _raw_stream(stream, residual))
     if rc:
@@ -171,27 +193,29 @@ def linear(x, weight, bias=None, *, activation: str | None = None, residual=None
     mx = isinstance(x, (tuple, list))
     if mx != isinstance(weight, (tuple, list)):
         raise ReplaySSMError("x and weight: both are MX pairs or neither")
-    xs, ws = (x[0], weight[0]) if mx and len(x) and len(weight) else (x, weight)
-    if not isinstance(xs, torch.Tensor) or xs.dim() != 2 or not isinstance(ws, torch.Tensor) or ws.dim() != 2:
+    xs, ws = (x[0], weight[0]) if mx and x and weight else (x, weight)
+    dev = _device(xs, "x")
+    if xs.dim() != 2 or not isinstance(ws, torch.Tensor) or ws.dim() != 2:
         raise ReplaySSMError("x and weight: expected [rows, n_in] and [n_out, n_in]")
     rows, n_in = xs.shape
     n_out = ws.shape[0]
     if mx:
         _blocks(n_in, "x")
-        xp, xsp = _mx(x, rows, n_in, "x")
-        wp, wsp = _mx(weight, n_out, n_in, "weight")
+        xp, xsp = _mx(x, rows, n_in, dev, "x")
+        wp, wsp = _mx(weight, n_out, n_in, dev, "weight")
         pitch, ty = n_in, FP8_E4M3
-        _device(xs, x[1], *weight)
     else:
-        pitch = _pitch(x, (rows,), n_in, torch.bfloat16, "x")
-        xp, xsp, wsp, ty = x.data_ptr(), None, None, BF16
-        wp = _dense(weight, (n_out, n_in), torch.bfloat16, "weight")
-        _device(xs, weight)
-    bp = None if bias is None else _dense(bias, (n_out,), torch.float32, "bias")
+        if xs.dtype is torch.bfloat16 and xs.is_contiguous():
+            pitch = n_in
+        else:
+            pitch = _pitch(xs, (rows,), n_in, torch.bfloat16, "x")
+        xp, xsp, wsp, ty = xs.data_ptr(), None, None, BF16
+        wp = _at(weight, (n_out, n_in), torch.bfloat16, dev, "weight")
+    bp = None if bias is None else _at(bias, (n_out,), torch.float32, dev, "bias")
     rp, rt = None, NONE
     if residual is not None:
-        rt = _float(residual, "residual")
-        rp = _dense(residual, (rows, n_out), residual.dtype, "residual")
+        rt = _type(residual, "residual")
+        rp = _at(residual, (rows, n_out), residual.dtype, dev, "residual")
     if out is not None:
         out_dtype = _E4M3 if isinstance(out, (tuple, list)) else out.dtype
     ot = _OUT_TYPES.get(out_dtype)
@@ -199,13 +223,13 @@ def linear(x, weight, bias=None, *, activation: str | None = None, residual=None
         raise ReplaySSMError(f"out: bfloat16, float32 or an MX pair (float8_e4m3fn), got {out_dtype}")
     if ot == FP8_E4M3:
         _blocks(n_out, "out")
-        out, (op, osp) = _mx_out(out, rows, n_out, xs.device, stream)
-        _device(xs, bias, residual, *out)
+        if out is None:
+            out = _mx_empty(rows, n_out, xs.device, stream)
+        op, osp = _mx(out, rows, n_out, dev, "out")
     else:
         if out is None:
             out = _empty((rows, n_out), out_dtype, xs.device, stream)
-        op, osp = _dense(out, (rows, n_out), out_dtype, "out"), None
-        _device(xs, bias, residual, out)
+        op, osp = _at(out, (rows, n_out), out_dtype, dev, "out"), None
     d = RssmLinearDesc(rows, n_in, n_out, ty, ot, rt, act, scale)
     io = RssmLinearIO(xp, pitch, xsp, wp, wsp, bp, rp, op, osp)
     rc = _lib().replayssm_linear(ctypes.addressof(d), ctypes.addressof(io), _raw_stream(stream, xs))

@@ -98,6 +98,19 @@ def test_rows_in_8_bits_refuse(m):
     assert an(c=None) == -1 and an(s=None) == -1 and an(c=1) == -1 and an(rows=0) == 0
 
 
+def _device_tensors(monkeypatch):
+    """Tensors that say they are on device 0, the current one (nothing is launched)."""
+    class Dev(torch.Tensor):
+        is_cuda = True
+        at = 0
+
+        def get_device(self):
+            return self.at
+    from state_space_recurrence_amd import projection
+    monkeypatch.setattr(projection, "_current_device", lambda: 0)
+    return lambda t: t.as_subclass(Dev)
+
+
 def test_binding_refuses(rs):
     """Shapes, types, devices and pairs are checked before the library is called."""
     E = rs.ReplaySSMError
@@ -105,10 +118,9 @@ def test_binding_refuses(rs):
     pair = lambda n, k: (torch.zeros(n, k, dtype=torch.float8_e4m3fn),  # noqa: E731
                          torch.zeros(n, k // 32, dtype=torch.float8_e8m0fnu))
     for match, args, kw in (
-            ("activation", (x, w), dict(activation="tanh")), ("x:", (x, w), {}), ("pairs", (x, pair(96, 64)), {}),
-            ("pairs", (pair(2, 64), w), {}), ("n_in", (x[0], w), {}), ("n_in", ((), ()), {}), ("n_in", (x, None), {}),
-            ("multiple of 32", (pair(2, 48), pair(96, 48)), {}), ("codes", (pair(2, 64), pair(96, 64)), {}),
-            ("pair", (pair(2, 64) + (x,), pair(96, 64)), {})):
+            ("activation", (x, w), dict(activation="tanh")), ("x: expected a device", (x, w), {}),
+            ("pairs", (x, pair(96, 64)), {}), ("pairs", (pair(2, 64), w), {}), ("x: expected", ((), ()), {}),
+            ("x: expected", (None, None), {}), ("x: expected a device", (pair(2, 64), pair(96, 64)), {})):
         with pytest.raises(E, match=match):
             rs.linear(*args, **kw)
     for bad in (torch.zeros(64), torch.zeros(2, 48), torch.zeros(2, 64), torch.zeros(2, 64, dtype=torch.float16)):
@@ -120,43 +132,59 @@ def test_binding_refuses(rs):
             rs.add_norm_mx(bad, bad, torch.ones(64))
 
 
-def test_binding_refuses_behind_the_device_check(rs, m, monkeypatch):
-    """What is refused once the operands themselves are device tensors (device check aside)."""
-    class Dev(torch.Tensor):
-        is_cuda = True
-    mk = lambda t: t.as_subclass(Dev)  # noqa: E731
-    monkeypatch.setattr(m, "_device", lambda *t: None)
+def test_binding_refuses_device_tensors(rs, monkeypatch):
+    """What is refused once the operands themselves are device tensors."""
+    mk = _device_tensors(monkeypatch)
     E = rs.ReplaySSMError
     x, w = mk(torch.zeros(2, 64, dtype=BF16)), mk(torch.zeros(96, 64, dtype=BF16))
     f = lambda *s: mk(torch.zeros(*s))  # noqa: E731
-    for match, kw in (("bias", dict(bias=f(95))), ("bias", dict(bias=f(96).to(BF16))),
+    e4, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    pair = lambda n, k: (f(n, k).to(e4), f(n, k // 32).to(e8))  # noqa: E731
+    for match, kw in (("bias", dict(bias=f(95))), ("bias", dict(bias=f(96).to(BF16))), ("bias", dict(bias=torch.zeros(96))),
                       ("residual", dict(residual=f(2, 95))), ("residual", dict(residual=f(2, 96).to(torch.float16))),
                       ("out", dict(out=f(2, 95))), ("out", dict(out_dtype=torch.float16)),
-                      ("out", dict(out=f(2, 96).to(torch.float8_e4m3fn))), ("pair", dict(out=(f(2, 96),))),
-                      ("out codes", dict(out=(f(2, 96), f(2, 3))))):
+                      ("out", dict(out=f(2, 96).to(e4))), ("pair", dict(out=(f(2, 96),))),
+                      ("out codes", dict(out=(f(2, 96), f(2, 3)))), ("out scales", dict(out=(f(2, 96).to(e4), f(2, 3))))):
         with pytest.raises(E, match=match):
             rs.linear(x, w, **kw)
+    for match, args in (("n_in", (f(64).to(BF16), w)), ("n_in", (x, f(64).to(BF16))), ("n_in", (x, None)),
+                        ("x:", (f(2, 64), w)), ("weight", (x, f(96, 64))), ("weight", (x, f(96, 32).to(BF16))),
+                        ("multiple of 32", (pair(2, 48), pair(96, 48))), ("pair", (pair(2, 64) + (x,), pair(96, 64))),
+                        ("x codes", ((x, f(2, 2).to(e8)), pair(96, 64))), ("x scales", ((pair(2, 64)[0], f(2, 2)), pair(96, 64))),
+                        ("weight scales", (pair(2, 64), (pair(96, 64)[0], f(95, 2).to(e8))))):
+        with pytest.raises(E, match=match):
+            rs.linear(*args)
     with pytest.raises(E, match="multiple of 32"):
-        rs.linear(x, mk(torch.zeros(95, 64, dtype=BF16)), out_dtype=torch.float8_e4m3fn)
+        rs.linear(x, mk(torch.zeros(95, 64, dtype=BF16)), out_dtype=e4)
     with pytest.raises(E, match="weight"):
         rs.linear(x, mk(torch.zeros(96, 128, dtype=BF16))[:, ::2])
     with pytest.raises(E, match="strides"):
         rs.linear(mk(torch.zeros(2, 128, dtype=BF16))[:, ::2], w)
     with pytest.raises(E, match="residual_out"):
         rs.add_norm_mx(None, f(2, 64), f(64), residual_out=f(2, 64))
+    with pytest.raises(E, match="residual_out"):
+        rs.add_norm_mx(None, f(2, 64), f(64), post_weight=f(64))
+    for bad in (dict(y=f(2, 32)), dict(y=f(2, 64).to(torch.float16)), dict(y=torch.zeros(2, 64)), dict(y=f(1, 128)),
+                dict(weight=f(63)), dict(z=f(2, 128)[:, ::2])):
+        with pytest.raises(E):
+            rs.gated_norm_mx(**{**dict(y=f(2, 64), z=f(2, 64), weight=f(64)), **bad})
+    for bad in (dict(x=f(2, 32)), dict(x=f(2, 64).to(torch.float16)), dict(residual_out=f(2, 64).to(BF16)),
+                dict(post_weight=f(32)), dict(residual=f(2, 128)[:, ::2])):
+        with pytest.raises(E):
+            rs.add_norm_mx(**{**dict(x=f(2, 64), residual=f(2, 64), weight=f(64)), **bad})
 
 
-def test_tensors_of_two_devices_are_refused(rs, m, monkeypatch):
-    class On(torch.Tensor):
-        at = 0
-
-        def get_device(self):
-            return self.at
-    a, b = torch.zeros(1).as_subclass(On), torch.zeros(1).as_subclass(On)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    m._device(a, None, b)
+def test_tensors_of_other_devices_are_refused(rs, monkeypatch):
+    mk = _device_tensors(monkeypatch)
+    x, w, b = mk(torch.zeros(2, 64, dtype=BF16)), mk(torch.zeros(96, 64, dtype=BF16)), mk(torch.zeros(96))
     b.at = 1
-    with pytest.raises(rs.ReplaySSMError, match="one device"):
-        m._device(a, b)
-    with pytest.raises(rs.ReplaySSMError, match="current"):
-        m._device(b)
+    with pytest.raises(rs.ReplaySSMError, match="bias: is on device 1"):
+        rs.linear(x, w, b)
+    x.at = 1
+    with pytest.raises(rs.ReplaySSMError, match="not the current"):
+        rs.linear(x, w)
+    r = mk(torch.zeros(2, 64))
+    with pytest.raises(rs.ReplaySSMError, match="x: is on device 1"):
+        rs.add_norm_mx(x, r, mk(torch.zeros(64)))
+    with pytest.raises(rs.ReplaySSMError, match="y: expected"):
+        rs.gated_norm_mx(x, r, mk(torch.zeros(64)))
