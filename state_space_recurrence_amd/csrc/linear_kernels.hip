@@ -2,19 +2,30 @@
 // and w [N, K] in bf16 or in MX (E4M3 codes, a power of two per 32 elements).
 //
 // The weights are the matrix instruction's first operand, so an accumulator
-// holds 4 consecutive outputs of one row per lane: stores and the residual's
-// loads are wide, and a 32 x 32 tile's column of outputs, half in a lane and
-// half in lane ^ 32, is one block of an MX output.
+// holds 4 consecutive outputs of one row per lane.  A step is 128 bytes of K of
+// every row: 64 bf16 elements (four 32x32x16 products per 32 x 32 tile) or 128
+// codes.  Lane l of an operand holds row l % 32; its 16-byte chunk s of a step is
+// chunk 2 s + l / 32 of the row's 8 for both types.  In LDS chunk c of row r lies
+// at place c ^ (r >> 1 & 7): the 16 lanes that read at a time then touch all 64
+// banks (with r & 7 half of them: a third of the LDS cycles were conflicts).
 //
-// A step is 128 bytes of K of every row: 64 bf16 elements (four 32x32x16
-// products per 32 x 32 tile) or 128 codes (two scaled 32x32x64 products).  Lane
-// l of an operand holds row l % 32; its 16-byte chunk s of a step is chunk
-// 2 s + l / 32 of the row's 8 for both types: one MX product takes two of them,
-// and its scale is byte 2 t + l / 32 of the row's four of the step (t the
-// product).  In LDS chunk c of row r lies at place c ^ (r & 7), so that the 8
-// lanes that read at a time touch all banks.
+// MX operands are multiplied in one of two ways.  Scaled 8-bit products (two
+// 32x32x64 per tile and step) run at twice the bf16 rate, but the matrix units
+// cut each product 13 binary places below the largest of those that they add at
+// once: sums are off by about 2^-14 of their terms, which bf16 outputs (2^-9)
+// hide.  fp32 and MX outputs are made of operands widened to bf16, which is
+// exact, so their sums are those of bf16 rows.  Sums are fp32.
 //
-// Sums are fp32.  A product of a zero code with a NaN is NaN as elsewhere.
+// What bounds it (M rows, 14432 outputs of 4096 inputs unless said otherwise):
+//   - one row: the weights' bytes; 23 us for 118 MB of bf16, 5.1 TB/s.
+//   - tens of rows: loads in flight.  A compute unit keeps about 110 of its L1's
+//     requests (128 bytes) on their way; 64 rows take 27 us in bf16, 18 in MX.
+//   - hundreds: the same: 256 rows 47 us in bf16, 30 in MX.
+//   - thousands: power.  The clock falls to 1.6 GHz (bf16) or 1.7 (MX), with the
+//     matrix units busy 81 % and 73 % of its cycles: 8192^3 takes 865 us (1.27
+//     PFLOP/s) and 475 us (2.3).  With all loads from L2 they are busy 98 % and the
+//     clock falls to 1.4: 834 us.  Tiles that stay with a workgroup, the next one's
+//     loads behind the stores of the last, measured the same and were dropped.
 #include "linear.h"
 
 #include "mixer_device.h"
@@ -176,17 +187,25 @@ __device__ __forceinline__ void multiply(f16v (&acc)[TM][TN], const operand (&w)
     }
 }
 
-// Rows 0..31 of `tile` (LDS, at a multiple of 16 rows) as an operand, with the
-// step's scales of a row every `at_row` bytes.
-template <Product PR>
-__device__ __forceinline__ operand read_operand(const char *tile, const char *scales, int at_row, int lane) {
-    operand o;
+// A row's four scales of a step: the dword at `at`, or (not WHOLE) bytes shift % 4
+// .. + 3 of it and the one a plane behind it, `left` of them inside the row (zeros
+// behind it).
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t row_scales(const char *at, int plane, int shift, int left) {
+    uint32_t v = *reinterpret_cast<const uint32_t *>(at);
+    if constexpr (!WHOLE) {
+        v = __builtin_amdgcn_alignbyte(*reinterpret_cast<const uint32_t *>(at + plane), v, shift);
+        if (left < 4) v &= (1u << (8 * left)) - 1;
+    }
+    return v;
+}
+
+// Rows 0..31 of `tile` (LDS, at a multiple of 16 rows) as an operand, but for its scales.
+__device__ __forceinline__ void read_chunks(operand &o, const char *tile, int lane) {
     const int r = lane & 31, h = lane >> 5;
     const char *p = tile + r * kStep;
 #pragma unroll
     for (int s = 0; s < 4; ++s) o.c[s] = *reinterpret_cast<const u4v *>(p + (((2 * s + h) ^ ((r >> 1) & 7)) << 4));
-    o.scales = PR == BF16 ? 0 : *reinterpret_cast<const uint32_t *>(scales + r * at_row) >> (PR == MX_FAST ? 8 * h : 0);
-    return o;
 }
 
 // ----------------------------------------------------- rows of any alignment --
@@ -259,8 +278,13 @@ __global__ void __launch_bounds__(256) linear_any_kernel(LinearParams p) {
     for (int k = 0; k < steps; ++k) {
         if (k + 1 < steps) load(k + 1);
         __syncthreads();
-        const operand w[1] = {read_operand<MX ? MX_EXACT : BF16>(&tile[k & 1][wn * kStep], reinterpret_cast<const char *>(&scales[k & 1][wn]), 4, lane)};
-        const operand x[1] = {read_operand<MX ? MX_EXACT : BF16>(&tile[k & 1][wm * kStep], reinterpret_cast<const char *>(&scales[k & 1][wm]), 4, lane)};
+        operand w[1], x[1];
+        read_chunks(w[0], &tile[k & 1][wn * kStep], lane);
+        read_chunks(x[0], &tile[k & 1][wm * kStep], lane);
+        if constexpr (MX) {
+            w[0].scales = scales[k & 1][wn + (lane & 31)];
+            x[0].scales = scales[k & 1][wm + (lane & 31)];
+        }
         multiply<MX ? MX_EXACT : BF16>(acc, w, x);
         if (k + 1 < steps) put((k + 1) & 1);
     }
@@ -326,8 +350,13 @@ __device__ __forceinline__ void tile_of(unsigned id, unsigned tiles_n, unsigned 
     tm = band * GROUP + in - tn * high;
 }
 
+// A byte offset outside every buffer here: a load from it brings zeros (with a
+// scalar offset inside the buffer, as the range check may take that off its size).
+constexpr int kNowhere = 0x7FFFFFF0;
+
 // One side's rows of a tile, on their way to LDS: ROWS rows by WAVES waves, a
-// load of eight rows each.  Rows behind the last are the last again.
+// load of eight rows each.  Rows behind the last are the last again; chunks
+// behind a row's end are zeros.
 template <int ROWS, int WAVES>
 struct RowLoads {
     static constexpr int kLoads = ROWS / 8 / WAVES;
@@ -338,14 +367,52 @@ struct RowLoads {
         const int last = (int)min((int64_t)ROWS, count - first) - 1;
         rows = resource(static_cast<const char *>(p) + first * pitch, (int)(last * pitch) + k_bytes);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = 8 * (wave + i * WAVES) + lane / 8;
-            off[i] = min(r, last) * (int)pitch + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+        for (int i = 0; i < kLoads; ++i) off[i] = min(row_of(i, wave, lane), last) * (int)pitch + 16 * chunk_of(i, wave, lane);
+    }
+    static __device__ __forceinline__ int row_of(int i, int wave, int lane) { return 8 * (wave + i * WAVES) + lane / 8; }
+    static __device__ __forceinline__ int chunk_of(int i, int wave, int lane) {
+        return (lane & 7) ^ ((row_of(i, wave, lane) >> 1) & 7);
+    }
+    // `left`: bytes of a row from step k on.
+    __device__ __forceinline__ void issue(int k, int left, unsigned lds, int wave, int lane) const {
+        if (left >= kStep) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) load_to_lds16(rows, off[i], k * kStep, lds + 1024 * (wave + i * WAVES));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                load_to_lds16(rows, 16 * chunk_of(i, wave, lane) < left ? off[i] : kNowhere, k * kStep,
+                              lds + 1024 * (wave + i * WAVES));
         }
     }
-    __device__ __forceinline__ void issue(int k, unsigned lds, int wave) const {
+};
+
+// The scales of 64 rows of one side (a lane each) on their way to LDS, for four
+// steps at a time.  Rows of whole fours: 16 bytes a row, at_row = 16 bytes apart,
+// the steps' at_step = 4 bytes within them.  Other rows may start at any byte:
+// five planes of a dword a row (at_row = 4, at_step = a plane), of which a step's
+// four bytes lie in two neighbouring ones; dwords behind the tile's last are that
+// one again.
+struct ScaleLoads {
+    u4v rows;
+    int off, end;
+    __device__ __forceinline__ ScaleLoads() {}
+    // Lane's row `row` of those from `first` on, of which `last` is the last to be read.
+    __device__ __forceinline__ ScaleLoads(const uint8_t *scales, int per, int64_t first, int last, int row) {
+        const int64_t start = first * per, base = start & ~(int64_t)3;
+        const int shift = (int)(start - base);
+        end = (shift + (last + 1) * per - 1) & ~3;
+        rows = resource(scales + base, end + 4);
+        off = (shift + min(row, last) * per) & ~3;
+    }
+    template <bool WHOLE>
+    __device__ __forceinline__ void issue(int g, int steps, unsigned to, int plane) const {
+        if constexpr (WHOLE) {
+            load_to_lds16(rows, off, 16 * min(g, steps / 4 - 1), to);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) load_to_lds16(rows, off[i], k * kStep, lds + 1024 * (wave + i * WAVES));
+            for (int s = 0; s < 5; ++s) load_to_lds4(rows, min(off + 16 * g + 4 * s, end), 0, to + s * plane);
+        }
     }
 };
 
@@ -356,13 +423,14 @@ struct RowLoads {
 // step that it holds in registers, the other reads its next operands, so the
 // matrix cores always have one of them to work for.  Chunk c of row r of a half
 // step lies at place c ^ (r >> 2 & 3) of its 64 bytes.
-template <Product PR>
+template <Product PR, bool WHOLE>
 __global__ void __launch_bounds__(512) linear_wide_kernel(LinearParams p) {
     constexpr int B = 256, kHalf = kStep / 2, kSide = B * kHalf, kStages = 4;
     constexpr int kLoads = 4;   // of a wave and half step
-    constexpr int kGroup = 8;   // half steps whose scales (16 bytes a row) are loaded together
+    constexpr int kGroup = 8;   // half steps whose scales are loaded together
     __shared__ __attribute__((aligned(1024))) char tile[kStages][2 * kSide];
-    __shared__ __attribute__((aligned(1024))) char scales[2][PR == BF16 ? 16 : 2 * B * 16];
+    constexpr int kGroupBytes = PR == BF16 ? 16 : 2 * B * 20;
+    __shared__ __attribute__((aligned(1024))) char scales[2][kGroupBytes];
     unsigned tn, tm;
     tile_of<8>(blockIdx.x, (p.n_out + B - 1) / B, (unsigned)((p.rows + B - 1) / B), tn, tm);
     const int n0 = tn * B;
@@ -380,36 +448,35 @@ __global__ void __launch_bounds__(512) linear_wide_kernel(LinearParams p) {
         ow[i] = min(r, last_n) * (int)p.w_pitch + 16 * c;
         ox[i] = min(r, last_m) * (int)p.x_pitch + 16 * c;
     }
-    u4v rs = (u4v)0u;
-    int os = 0;
+    const int per = p.k_bytes / kMxBlock;
+    ScaleLoads sc;
     if constexpr (PR != BF16) {   // waves 0..3 load the scales of w's rows, 4..7 those of x's
-        const int per = p.k_bytes / kMxBlock, last = wave < 4 ? last_n : last_m;
-        rs = resource(wave < 4 ? p.w_scales + (int64_t)n0 * per : p.x_scales + m0 * per, (last + 1) * per);
-        os = min(64 * (wave & 3) + lane, last) * per;
+        const int row = 64 * (wave & 3) + lane;
+        sc = wave < 4 ? ScaleLoads(p.w_scales, per, n0, last_n, row) : ScaleLoads(p.x_scales, per, m0, last_m, row);
     }
     const unsigned lds = lds_offset(tile), lds_sc = lds_offset(scales);
-    const int halves = p.k_bytes / kHalf;
-    // Rows whose scales are whole groups: 16 bytes of a row together.  Others: the groups' steps one after the other.
-    const bool whole = halves % kGroup == 0;
-    const int at_row = whole ? 16 : 4, at_step = whole ? 4 : 8 * B;
+    const int steps = (p.k_bytes + kStep - 1) / kStep, halves = (p.k_bytes + kHalf - 1) / kHalf;
+    constexpr int at_row = WHOLE ? 16 : 4, at_step = WHOLE ? 4 : 8 * B;   // (see ScaleLoads)
     const auto issue_scales = [&](int g) {
-        const unsigned to = lds_sc + (g & 1) * 32 * B + 64 * at_row * wave;
-        if (whole) {
-            load_to_lds16(rs, os, 16 * min(g, halves / kGroup - 1), to);
-        } else {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) load_to_lds4(rs, os, 4 * min(4 * g + s, halves / 2 - 1), to + s * at_step);
-        }
+        sc.template issue<WHOLE>(g, steps, lds_sc + (g & 1) * kGroupBytes + 64 * at_row * wave, at_step);
     };
     // Behind the end the last half step is loaded again, for nobody: a constant number of loads is in flight.
     const auto issue = [&](int j) {
-        const int at = min(j, halves - 1) * kHalf;
+        const int at = min(j, halves - 1) * kHalf, left = p.k_bytes - at;
         const unsigned to = lds + (j & 3) * 2 * kSide + 1024 * wave;
-        load_to_lds16(rw, ow[0], at, to);
-        load_to_lds16(rw, ow[1], at, to + 8192);
-        load_to_lds16(rx, ox[0], at, to + kSide);
-        load_to_lds16(rx, ox[1], at, to + kSide + 8192);
-        if constexpr (PR != BF16)   // (in time for half step j - j % 8 + 8; the waits below count four loads, at most one too few)
+        const auto load = [&](int w0, int w1, int x0, int x1) {
+            load_to_lds16(rw, w0, at, to);
+            load_to_lds16(rw, w1, at, to + 8192);
+            load_to_lds16(rx, x0, at, to + kSide);
+            load_to_lds16(rx, x1, at, to + kSide + 8192);
+        };
+        if (left >= kHalf) {
+            load(ow[0], ow[1], ox[0], ox[1]);
+        } else {   // chunks behind a row's end are zeros
+            const bool in = 16 * ((lane & 3) ^ ((lane >> 4) & 3)) < left;
+            load(in ? ow[0] : kNowhere, in ? ow[1] : kNowhere, in ? ox[0] : kNowhere, in ? ox[1] : kNowhere);
+        }
+        if constexpr (PR != BF16)   // (in time for half step j - j % 8 + 8; the waits below count four loads a half step and wait for more where these are between)
             if ((j & (kGroup - 1)) == 3) issue_scales(j / kGroup + 1);
     };
 
@@ -434,12 +501,14 @@ __global__ void __launch_bounds__(512) linear_wide_kernel(LinearParams p) {
                 w[i][s] = *reinterpret_cast<const u4v *>(t + (wn + 32 * i) * kHalf + (place ^ (32 * s)));
         }
         if constexpr (PR != BF16) {   // MX_FAST: the lane's one scale in byte 0; MX_EXACT: of chunks s = 0, 1 in bytes 0, 1
-            const char *sc = scales[(j / kGroup) & 1] + at_step * ((j >> 1) & 3) + r * at_row;
-            const int shift = 16 * (j & 1) + (PR == MX_FAST ? 8 * h : 0);
+            const char *at = scales[(j / kGroup) & 1] + at_step * ((j >> 1) & 3) + r * at_row;
+            const int left = per - 2 * (j & ~1), shift = 16 * (j & 1) + (PR == MX_FAST ? 8 * h : 0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) sx[i] = *reinterpret_cast<const uint32_t *>(sc + (B + wm + 32 * i) * at_row) >> shift;
+            for (int i = 0; i < 2; ++i)
+                sx[i] = row_scales<WHOLE>(at + (B + wm + 32 * i) * at_row, at_step, ((int)m0 + wm + 32 * i + r) * per, left) >> shift;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sw[i] = *reinterpret_cast<const uint32_t *>(sc + (wn + 32 * i) * at_row) >> shift;
+            for (int i = 0; i < 4; ++i)
+                sw[i] = row_scales<WHOLE>(at + (wn + 32 * i) * at_row, at_step, (n0 + wn + 32 * i + r) * per, left) >> shift;
         }
     };
     const auto work = [&] {
@@ -517,11 +586,11 @@ __global__ void __launch_bounds__(512) linear_wide_kernel(LinearParams p) {
 
 // BN outputs x BM rows by WN x WM waves, STAGES steps in LDS: every wave asks for
 // step k + STAGES - 1 before it multiplies step k.
-template <Product PR, int BN, int BM, int WN, int WM, int STAGES>
+template <Product PR, bool WHOLE, int BN, int BM, int WN, int WM, int STAGES>
 __global__ void __launch_bounds__(64 * WN * WM) linear_tile_kernel(LinearParams p) {
     constexpr int kWaves = WN * WM, TN = BN / WN / 32, TM = BM / WM / 32, kRows = BN + BM, kStage = kRows * kStep;
     constexpr int kLoads = kRows / 8 / kWaves, kScaleLoads = PR == BF16 ? 0 : (kRows / 64 + kWaves - 1) / kWaves;
-    constexpr int kScaleFour = PR == BF16 ? 16 : kRows * 16;   // bytes of four steps' scales
+    constexpr int kScaleFour = PR == BF16 ? 16 : kRows * 20;   // bytes of four steps' scales
     static_assert(STAGES <= 5, "a four's scales are asked for no later than its first step");
     static_assert(kRows / 8 % kWaves == 0 && BN % 64 == 0 && BM % 64 == 0, "whole loads");
     static_assert(STAGES * kStage >= kWaves * TN * 4096, "sums pass through the stages");
@@ -534,52 +603,41 @@ __global__ void __launch_bounds__(64 * WN * WM) linear_tile_kernel(LinearParams 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const RowLoads<BN, kWaves> lw(p.w, p.w_pitch, n0, p.n_out, p.k_bytes, wave, lane);
     const RowLoads<BM, kWaves> lx(p.x, p.x_pitch, m0, p.rows, p.k_bytes, wave, lane);
-    const int steps = p.k_bytes / kStep;
-    // Scales come for four steps together where rows have whole fours (see the wide tiles).
-    const bool whole = steps % 4 == 0;
-    const int at_row = whole ? 16 : 4, at_step = whole ? 4 : 4 * kRows;
+    const int steps = (p.k_bytes + kStep - 1) / kStep, per = p.k_bytes / kMxBlock;
+    constexpr int at_row = WHOLE ? 16 : 4, at_step = WHOLE ? 4 : 4 * kRows;   // (see ScaleLoads)
     // Few rows: the weights are read once, by tiles side by side, which start 12
     // steps apart and go round, so that they do not all ask the same channels for
     // the same part of K (64 rows of 14432 x 4096: 29.6 -> 27.1 us).  Tiles that share
     // weights stay together (1024 rows of 4096 x 6144: 63 us, apart 70).
-    const bool apart = whole && p.rows <= BM;
+    const bool apart = p.k_bytes % (4 * kStep) == 0 && p.rows <= BM;
     const int start = apart ? 4 * (3 * tn % (steps / 4)) : 0;
-    u4v sc[kScaleLoads ? kScaleLoads : 1];
-    int soff[kScaleLoads ? kScaleLoads : 1], sto[kScaleLoads ? kScaleLoads : 1];
+    ScaleLoads sc[kScaleLoads ? kScaleLoads : 1];
+    int sto[kScaleLoads ? kScaleLoads : 1];
     if constexpr (PR != BF16) {   // 64 rows' scales a load: w's, then x's (waves without rows load others' again)
-        const int per = p.k_bytes / kMxBlock;
 #pragma unroll
         for (int i = 0; i < kScaleLoads; ++i) {
             const int at = 64 * ((wave + i * kWaves) % (kRows / 64));
             const bool ofw = at < BN;
-            const int64_t row0 = ofw ? n0 : m0;
-            const int last = (int)min((int64_t)(ofw ? BN : BM), (ofw ? (int64_t)p.n_out : p.rows) - row0) - 1;
-            sc[i] = resource((ofw ? p.w_scales : p.x_scales) + row0 * per, (last + 1) * per);
-            soff[i] = min(at - (ofw ? 0 : BN) + lane, last) * per;
+            const int64_t first = ofw ? n0 : m0;
+            const int last = (int)min((int64_t)(ofw ? BN : BM), (ofw ? (int64_t)p.n_out : p.rows) - first) - 1;
+            sc[i] = ScaleLoads(ofw ? p.w_scales : p.x_scales, per, first, last, at - (ofw ? 0 : BN) + lane);
             sto[i] = at * at_row;
         }
     }
     const unsigned lds = lds_offset(tile), lds_sc = lds_offset(scales);
     const auto issue_scales = [&](int g) {
+        int at = min(g, (steps - 1) / 4) + start / 4;
+        at = at > (steps - 1) / 4 ? at - steps / 4 : at;
 #pragma unroll
-        for (int i = 0; i < kScaleLoads; ++i) {
-            const unsigned to = lds_sc + (g & 1) * kScaleFour + sto[i];
-            if (whole) {
-                const int at = min(g, steps / 4 - 1) + start / 4;
-                load_to_lds16(sc[i], soff[i], 16 * (at >= steps / 4 ? at - steps / 4 : at), to);
-            } else {
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    load_to_lds4(sc[i], soff[i], 4 * min(4 * g + s, steps - 1), to + s * at_step);
-            }
-        }
+        for (int i = 0; i < kScaleLoads; ++i) sc[i].template issue<WHOLE>(at, steps, lds_sc + (g & 1) * kScaleFour + sto[i], at_step);
     };
     // Steps behind the last are the last again (a constant number of loads is in flight); nothing reads them.
     const auto issue = [&](int k, int stage) {
         int at = min(k, steps - 1) + start;
         at = at >= steps ? at - steps : at;
-        lw.issue(at, lds + stage * kStage, wave);
-        lx.issue(at, lds + stage * kStage + BN * kStep, wave);
+        const int left = p.k_bytes - at * kStep;
+        lw.issue(at, left, lds + stage * kStage, wave, lane);
+        lx.issue(at, left, lds + stage * kStage + BN * kStep, wave, lane);
     };
     f16v acc[TM][TN];
 #pragma unroll
@@ -598,12 +656,21 @@ __global__ void __launch_bounds__(64 * WN * WM) linear_tile_kernel(LinearParams 
         issue(k + STAGES - 1, next);
         operand w[TN], x[TM];
         const char *t = tile[stage], *s = scales[(k >> 2) & 1] + (k & 3) * at_step;
+        const int left = per - 4 * k;   // (rows that start apart are whole)
 #pragma unroll
-        for (int j = 0; j < TM; ++j)
-            x[j] = read_operand<PR>(t + (BN + wm + 32 * j) * kStep, s + (BN + wm + 32 * j) * at_row, at_row, lane);
+        for (int j = 0; j < TM; ++j) read_chunks(x[j], t + (BN + wm + 32 * j) * kStep, lane);
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-            w[i] = read_operand<PR>(t + (wn + 32 * i) * kStep, s + (wn + 32 * i) * at_row, at_row, lane);
+        for (int i = 0; i < TN; ++i) read_chunks(w[i], t + (wn + 32 * i) * kStep, lane);
+        if constexpr (PR != BF16) {
+            const int r = lane & 31, shift = PR == MX_FAST ? 8 * (lane >> 5) : 0;
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+                x[j].scales = row_scales<WHOLE>(s + (BN + wm + 32 * j + r) * at_row, at_step,
+                                                ((int)m0 + wm + 32 * j + r) * per, left) >> shift;
+#pragma unroll
+            for (int i = 0; i < TN; ++i)
+                w[i].scales = row_scales<WHOLE>(s + (wn + 32 * i + r) * at_row, at_step, (n0 + wn + 32 * i + r) * per, left) >> shift;
+        }
         multiply<PR>(acc, w, x);
         stage = stage + 1 == STAGES ? 0 : stage + 1;
         next = next + 1 == STAGES ? 0 : next + 1;
@@ -652,13 +719,24 @@ __global__ void __launch_bounds__(64 * WAVES) linear_few_kernel(LinearParams p) 
         u4v c[2];
         uint32_t s;
     };
-    const int steps = p.k_bytes / kStep;
-    const auto load = [&](const char *v, const uint8_t *scales, int k) {   // behind the last step: zeros
+    const int steps = (p.k_bytes + kStep - 1) / kStep;
+    typedef uint32_t u1u __attribute__((aligned(1)));
+    const auto load = [&](const char *v, const uint8_t *scales, int k) {   // behind a row's end: zeros
         step o;
-        const bool in = k < steps;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) o.c[i] = in ? *reinterpret_cast<const u4v *>(v + k * kStep + 64 * i) : (u4v)0u;
-        o.s = MX && in ? *reinterpret_cast<const uint32_t *>(scales + 4 * k) : 0;
+        for (int i = 0; i < 2; ++i) {
+            const int at = k * kStep + 64 * i;
+            o.c[i] = at + 16 * q < p.k_bytes ? *reinterpret_cast<const u4v *>(v + at) : (u4v)0u;
+        }
+        o.s = 0;
+        if constexpr (MX) {
+            const int left = per - 4 * k;
+            if (left >= 4) o.s = *reinterpret_cast<const u1u *>(scales + 4 * k);
+            else
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (i < left) o.s |= (uint32_t)scales[4 * k + i] << (8 * i);
+        }
         return o;
     };
     for (int k = wave; k < steps; k += AHEAD * WAVES) {
@@ -748,7 +826,8 @@ Tile best_tile(const LinearParams &p, Product pr) {
     return (Tile)best;
 }
 
-template <Product PR>
+// WHOLE: rows of whole fours of steps' scales (bf16 rows have none).
+template <Product PR, bool WHOLE>
 void launch_direct(const LinearParams &p, hipStream_t s) {
     constexpr bool MX = PR != BF16;
     const Tile t = best_tile(p, PR);
@@ -757,13 +836,13 @@ void launch_direct(const LinearParams &p, hipStream_t s) {
         case T16: hipLaunchKernelGGL((linear_few_kernel<MX, 8, 1, 1, 2>), grid, dim3(512), 0, s, p); break;
         case T32x16: hipLaunchKernelGGL((linear_few_kernel<MX, 8, 2, 1, 2>), grid, dim3(512), 0, s, p); break;
         case T32: hipLaunchKernelGGL((linear_few_kernel<MX, 8, 2, 2, 2>), grid, dim3(512), 0, s, p); break;
-        case T64: hipLaunchKernelGGL((linear_tile_kernel<PR, 64, 64, 2, 2, 4>), grid, dim3(256), 0, s, p); break;
+        case T64: hipLaunchKernelGGL((linear_tile_kernel<PR, WHOLE, 64, 64, 2, 2, 4>), grid, dim3(256), 0, s, p); break;
         case T64x128:   // (MX_EXACT: never the least)
             if constexpr (PR != MX_EXACT)
-                hipLaunchKernelGGL((linear_tile_kernel<PR, 64, 128, 2, 2, 4>), grid, dim3(256), 0, s, p);
+                hipLaunchKernelGGL((linear_tile_kernel<PR, WHOLE, 64, 128, 2, 2, 4>), grid, dim3(256), 0, s, p);
             break;
-        case T128: hipLaunchKernelGGL((linear_tile_kernel<PR, 128, 128, 2, 4, 4>), grid, dim3(512), 0, s, p); break;
-        default: hipLaunchKernelGGL((linear_wide_kernel<PR>), grid, dim3(512), 0, s, p); break;
+        case T128: hipLaunchKernelGGL((linear_tile_kernel<PR, WHOLE, 128, 128, 2, 4, 4>), grid, dim3(512), 0, s, p); break;
+        default: hipLaunchKernelGGL((linear_wide_kernel<PR, WHOLE>), grid, dim3(512), 0, s, p); break;
     }
 }
 
@@ -772,19 +851,19 @@ bool multiple(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p)
 }  // namespace
 
 hipError_t launch_linear(const LinearParams &p, bool mx, hipStream_t s) {
-    // Whole steps at aligned addresses are loaded straight to LDS or operands.
-    const bool direct = p.k_bytes % kStep == 0 && p.x_pitch % 16 == 0 && multiple(p.x, 16) && multiple(p.w, 16) &&
+    // Rows at aligned addresses are loaded straight to LDS or operands.
+    const bool direct = p.w_pitch % 16 == 0 && p.x_pitch % 16 == 0 && multiple(p.x, 16) && multiple(p.w, 16) &&
                         (!mx || (multiple(p.x_scales, 4) && multiple(p.w_scales, 4)));
     if (!direct) {
         const dim3 grid((unsigned)tiles_of(p, 64, 64));
         if (mx) hipLaunchKernelGGL(linear_any_kernel<true>, grid, dim3(256), 0, s, p);
         else hipLaunchKernelGGL(linear_any_kernel<false>, grid, dim3(256), 0, s, p);
     } else if (!mx) {
-        launch_direct<BF16>(p, s);
-    } else if (p.out_type == RSSM_BF16) {
-        launch_direct<MX_FAST>(p, s);
+        launch_direct<BF16, true>(p, s);
     } else {
-        launch_direct<MX_EXACT>(p, s);
+        const bool whole = p.k_bytes % (4 * kStep) == 0;
+        if (p.out_type == RSSM_BF16) whole ? launch_direct<MX_FAST, true>(p, s) : launch_direct<MX_FAST, false>(p, s);
+        else whole ? launch_direct<MX_EXACT, true>(p, s) : launch_direct<MX_EXACT, false>(p, s);
     }
     return hipGetLastError();
 }

@@ -182,7 +182,8 @@ def test_norms_mx_agree_with_quantized_norms(rs):
 
 # rows x outputs x inputs: single rows, edges of every tile, sums of one step and of many
 SIZES = [(1, 1, 1), (1, 33, 64), (2, 16, 8), (3, 100, 63), (5, 7, 251), (16, 48, 128), (17, 130, 192), (31, 64, 1000),
-         (33, 96, 640), (64, 64, 64), (65, 257, 128), (100, 300, 320), (128, 128, 256), (129, 200, 72)]
+         (33, 96, 640), (64, 64, 64), (65, 257, 128), (100, 300, 320), (128, 128, 256), (129, 200, 72),
+         (1, 40, 8), (4, 100, 1000), (20, 200, 2056), (70, 500, 88)]
 
 
 @pytest.mark.parametrize("rows,n_out,n_in", SIZES)
@@ -193,7 +194,7 @@ def test_linear_bf16(rs, rows, n_out, n_in, out_type):
 
 MX_SIZES = [(1, 1, 32), (1, 33, 64), (2, 16, 96), (3, 100, 128), (5, 7, 256), (16, 48, 1152), (17, 130, 224),
             (31, 64, 1024), (33, 96, 640), (64, 64, 128), (65, 257, 384), (100, 300, 320), (128, 128, 256),
-            (129, 200, 160)]
+            (129, 200, 160), (1, 40, 1056), (4, 100, 992), (20, 200, 2080), (70, 500, 96)]
 
 
 @pytest.mark.parametrize("rows,n_out,n_in", MX_SIZES)
@@ -221,7 +222,12 @@ BY_TILE = [(BF16, 20, 4100, 576), (BF16, 32, 4128, 2048), (BF16, 33, 4100, 1024)
            (BF16, 65, 9000, 640), (BF16, 128, 9120, 2048), (BF16, 200, 9000, 1088), (BF16, 256, 9120, 2048),
            (BF16, 2000, 4100, 1088), (BF16, 2048, 4128, 2048), (MX, 20, 4100, 1152), (MX, 33, 4128, 2048),
            (MX, 64, 9000, 4096), (MX, 65, 9000, 1152), (MX, 128, 9120, 2048), (MX, 200, 9000, 1152),
-           (MX, 256, 9120, 2048), (MX, 2000, 4100, 1152), (MX, 3000, 4128, 2048)]
+           (MX, 256, 9120, 2048), (MX, 2000, 4100, 1152), (MX, 3000, 4128, 2048),
+           # rows that end inside a step, and scales that start at any byte
+           (BF16, 20, 4100, 1000), (BF16, 33, 4128, 1096), (BF16, 128, 9120, 8), (BF16, 200, 9000, 1048),
+           (BF16, 2000, 4128, 1112), (BF16, 2000, 4100, 1064), (MX, 20, 4100, 1184), (MX, 33, 4128, 1120), (MX, 64, 9000, 32),
+           (MX, 65, 9120, 1248), (MX, 128, 9000, 1216), (MX, 200, 9120, 1056), (MX, 250, 9000, 96), (MX, 2000, 4128, 1184),
+           (MX, 3000, 4128, 1120), (MX, 2000, 4100, 1056), (MX, 3000, 4100, 64)]
 
 
 @pytest.mark.parametrize("x_type,rows,n_out,n_in", BY_TILE)
@@ -250,7 +256,9 @@ def test_activation_values(rs, act):
 SHAPES_BY_KERNEL = [(BF16, 3, 100, 65), (BF16, 5, 96, 256), (BF16, 40, 160, 256), (BF16, 200, 544, 256), (MX, 5, 96, 256),
                     (MX, 9, 160, 96), (MX, 40, 160, 256), (MX, 200, 544, 256), (BF16, 600, 1000, 192), (MX, 600, 1000, 256),
                     (BF16, 33, 4100, 128), (BF16, 100, 9024, 192), (BF16, 200, 9024, 64), (BF16, 2000, 4128, 64),
-                    (MX, 33, 4100, 256), (MX, 200, 9024, 128), (MX, 3000, 4128, 128)]
+                    (MX, 33, 4100, 256), (MX, 200, 9024, 128), (MX, 3000, 4128, 128),
+                    (BF16, 5, 96, 72), (BF16, 33, 4100, 136), (BF16, 200, 9024, 88), (BF16, 2000, 4128, 72), (MX, 5, 96, 160),
+                    (MX, 33, 4100, 224), (MX, 200, 9024, 96), (MX, 3000, 4128, 160)]
 
 
 @pytest.mark.parametrize("x_type,rows,n_out,n_in", SHAPES_BY_KERNEL)
@@ -260,7 +268,7 @@ def test_nothing_else_is_written(rs, x_type, rows, n_out, n_in):
     xc = _cuda(x)
     if x_type == BF16:
         wide = torch.full((rows + 2, n_in + 64), math.nan, dtype=BF16, device="cuda")
-        wide[1:-1, 8:8 + n_in] = xc
+        wide[1:-1, 8:8 + n_in] = xc          # (a multiple of 8 elements: rows stay aligned where n_in is one)
         xc = wide[1:-1, 8:8 + n_in]
     buf = torch.full((rows + 4, n_out), 7.0, dtype=F32, device="cuda")
     rs.linear(xc, _cuda(w), out=buf[2:-2])
@@ -326,6 +334,18 @@ def test_unaligned_rows_agree(rs):
         view = flat.as_strided((50, 128), (pitch, 1), off)
         view.copy_(x.cuda())
         mixer_ref.assert_within(rs.linear(view, w.cuda(), out_dtype=F32), want, err, f"offset {off}")
+
+
+def test_scales_at_any_address(rs):
+    """MX scales that start between multiples of 4 bytes: the same values, by another kernel."""
+    x, w, xv, wv = _operands(MX, 50, 100, 96, 12)
+    want, err = ref.linear(xv, wv, None, None, None, 1.0)
+    xc, wc = _cuda(x), _cuda(w)
+    for off in (0, 1, 2, 3):
+        buf = torch.zeros(off + 150, dtype=torch.uint8, device="cuda")
+        scales = buf[off:].view(50, 3)
+        scales.copy_(xc[1].view(torch.uint8))
+        mixer_ref.assert_within(rs.linear((xc[0], scales.view(ref.E8M0)), wc, out_dtype=F32), want, err, f"offset {off}")
 
 
 def test_no_rows(rs):
