@@ -795,9 +795,10 @@ __global__ void __launch_bounds__(64 * WAVES) linear_few_kernel(LinearParams p) 
 // of 1 to 16384 rows of 256 to 16384 outputs; 1 is what 64 x 64 tiles take for one
 // round.  Small tiles keep all units at work, large ones load less for each
 // product: of 6144 inputs and 4096 outputs in bf16, 64 rows take 45 us in 16 x 16
-// tiles, 26 in 32 x 32, 34 in 64 x 64; 1024 rows 96 in 64 x 64, 63 in 128 x 128, 144
-// in 256 x 256; 8192 rows of 8192 x 8192 1560, 1125 and 862.
-enum Tile { T16, T32x16, T32, T64, T64x128, T128, T256, kTiles };
+// tiles, 26 in 32 x 32, 34 in 64 x 64; 1024 rows 96 in 64 x 64, 63 in 128 x 128, 94 in
+// 256 x 128, 144 in 256 x 256; 2048 rows 180, 128, 111 and 147; 8192 rows of 8192 x
+// 8192 1560, 1125, 1100 and 862.
+enum Tile { T16, T32x16, T32, T64, T64x128, T128, T256x128, T256, kTiles };
 struct TileCost {
     int n, m;
     float call[3], round[3];   // by Product
@@ -806,7 +807,7 @@ constexpr TileCost kTileCosts[kTiles] = {
     {16, 16, {.12f, .19f, .19f}, {.24f, .37f, .37f}},   {32, 16, {.14f, .23f, .23f}, {.42f, .56f, .56f}},
     {32, 32, {.13f, .16f, .16f}, {.48f, .81f, .81f}},   {64, 64, {.55f, .60f, .55f}, {.42f, .55f, .41f}},
     {64, 128, {.45f, 1e9f, .30f}, {.85f, .0f, .95f}}, {128, 128, {.40f, .0f, .45f}, {1.22f, 2.05f, 1.25f}},
-    {256, 256, {.0f, .0f, .15f}, {3.8f, 6.1f, 3.25f}},
+    {256, 128, {.0f, .0f, .15f}, {2.4f, 3.7f, 2.15f}},  {256, 256, {.0f, .0f, .15f}, {3.8f, 6.1f, 3.25f}},
 };
 
 int64_t tiles_of(const LinearParams &p, int n, int m) { return (p.rows + m - 1) / m * ((p.n_out + n - 1) / n); }
@@ -842,6 +843,7 @@ void launch_direct(const LinearParams &p, hipStream_t s) {
                 hipLaunchKernelGGL((linear_tile_kernel<PR, WHOLE, 64, 128, 2, 2, 4>), grid, dim3(256), 0, s, p);
             break;
         case T128: hipLaunchKernelGGL((linear_tile_kernel<PR, WHOLE, 128, 128, 2, 4, 4>), grid, dim3(512), 0, s, p); break;
+        case T256x128: hipLaunchKernelGGL((linear_tile_kernel<PR, WHOLE, 256, 128, 4, 2, 3>), grid, dim3(512), 0, s, p); break;
         default: hipLaunchKernelGGL((linear_wide_kernel<PR, WHOLE>), grid, dim3(512), 0, s, p); break;
     }
 }

@@ -220,14 +220,17 @@ def test_epilogue(rs, x_type, rows, n_out, n_in, bias, act, res_type, scale, out
 # and others, edges in both directions
 BY_TILE = [(BF16, 20, 4100, 576), (BF16, 32, 4128, 2048), (BF16, 33, 4100, 1024), (BF16, 64, 9000, 1088),
            (BF16, 65, 9000, 640), (BF16, 128, 9120, 2048), (BF16, 200, 9000, 1088), (BF16, 256, 9120, 2048),
+           (BF16, 700, 9000, 1088), (BF16, 700, 9024, 2048),
            (BF16, 2000, 4100, 1088), (BF16, 2048, 4128, 2048), (MX, 20, 4100, 1152), (MX, 33, 4128, 2048),
            (MX, 64, 9000, 4096), (MX, 65, 9000, 1152), (MX, 128, 9120, 2048), (MX, 200, 9000, 1152),
-           (MX, 256, 9120, 2048), (MX, 2000, 4100, 1152), (MX, 3000, 4128, 2048),
+           (MX, 256, 9120, 2048), (MX, 700, 9000, 1152), (MX, 700, 9024, 2048), (MX, 2000, 4100, 1152),
+           (MX, 3000, 4128, 2048),
            # rows that end inside a step, and scales that start at any byte
            (BF16, 20, 4100, 1000), (BF16, 33, 4128, 1096), (BF16, 128, 9120, 8), (BF16, 200, 9000, 1048),
            (BF16, 2000, 4128, 1112), (BF16, 2000, 4100, 1064), (MX, 20, 4100, 1184), (MX, 33, 4128, 1120), (MX, 64, 9000, 32),
            (MX, 65, 9120, 1248), (MX, 128, 9000, 1216), (MX, 200, 9120, 1056), (MX, 250, 9000, 96), (MX, 2000, 4128, 1184),
-           (MX, 3000, 4128, 1120), (MX, 2000, 4100, 1056), (MX, 3000, 4100, 64)]
+           (MX, 3000, 4128, 1120), (MX, 2000, 4100, 1056), (MX, 3000, 4100, 64),
+           (BF16, 700, 9024, 1032), (MX, 700, 9024, 1088), (MX, 690, 9000, 96)]
 
 
 @pytest.mark.parametrize("x_type,rows,n_out,n_in", BY_TILE)
@@ -258,7 +261,7 @@ SHAPES_BY_KERNEL = [(BF16, 3, 100, 65), (BF16, 5, 96, 256), (BF16, 40, 160, 256)
                     (BF16, 33, 4100, 128), (BF16, 100, 9024, 192), (BF16, 200, 9024, 64), (BF16, 2000, 4128, 64),
                     (MX, 33, 4100, 256), (MX, 200, 9024, 128), (MX, 3000, 4128, 128),
                     (BF16, 5, 96, 72), (BF16, 33, 4100, 136), (BF16, 200, 9024, 88), (BF16, 2000, 4128, 72), (MX, 5, 96, 160),
-                    (MX, 33, 4100, 224), (MX, 200, 9024, 96), (MX, 3000, 4128, 160)]
+                    (MX, 33, 4100, 224), (MX, 200, 9024, 96), (MX, 3000, 4128, 160), (BF16, 700, 9024, 72), (MX, 700, 9024, 96)]
 
 
 @pytest.mark.parametrize("x_type,rows,n_out,n_in", SHAPES_BY_KERNEL)
