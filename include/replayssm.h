@@ -466,7 +466,10 @@ int replayssm_add_norm(int64_t rows, int32_t dim, const void *x, int32_t x_dtype
  * with amax <= 448 scale, amax the largest finite size among the block's 32
  * elements (byte 0, 2^-127, at least, and for blocks of zeros); codes are
  * elements / scale rounded to nearest even; elements that are not finite become
- * NaN codes.  What they read may have any scale and codes (byte 255: NaN).
+ * NaN codes.  What they read may have any scale and codes (byte 255: NaN) whose
+ * values lie in fp32's range; values beyond it (scale bytes over 246) may count
+ * as infinities, and of values below 2^-126 what lies under 2^-133 may be lost
+ * (the last bits of codes below 2^-3 with scale bytes 0..2).
  * ------------------------------------------------------------------------ */
 
 /* Rows to MX: x [rows, dim] at x_pitch elements per row, F32 or BF16. */

@@ -339,6 +339,40 @@ def test_unaligned_rows_agree(rs):
         mixer_ref.assert_within(rs.linear(view, w.cuda(), out_dtype=F32), want, err, f"offset {off}")
 
 
+@pytest.mark.parametrize("rows,n_out,n_in", [(3, 64, 64), (64, 9000, 160), (200, 9024, 96), (2000, 4128, 64)])
+@pytest.mark.parametrize("sx,sw", [(0, 246), (1, 246), (3, 240), (60, 194), (246, 0), (246, 7), (127, 127)])
+def test_scales_over_their_range(rs, rows, n_out, n_in, sx, sw):
+    """From the least scale to the largest whose values are all finite: products of the codes times a power of two."""
+    g = _gen(sx)
+    xc, wc = (torch.randn(n, n_in, generator=g).mul(20).to(ref.E4M3) for n in (rows, n_out))
+    pair = lambda c, s: (c.cuda(), torch.full((c.shape[0], n_in // 32), s, dtype=torch.uint8, device="cuda").view(ref.E8M0))  # noqa: E731
+    for out_type in (F32, BF16):
+        got = rs.linear(pair(xc, sx), pair(wc, sw), out_dtype=out_type)
+        want, err = ref.linear(xc.cuda(), wc.cuda(), None, None, None, 1.0, cut=out_type == BF16)
+        f = 2.0 ** (sx + sw - 254)
+        # operands widened to bf16 are multiples of 2^-133, its least subnormal number: off by half of that, which is
+        # 2^-7 - s of a code with scale byte s, times the other side's codes; E4M3's codes are multiples of 2^-9, so this
+        # is nothing from byte 3 on
+        lost = lambda s: 2.0 ** (-7 - s) if s < 3 else 0.0  # noqa: E731
+        err = err + lost(sx) * wc.cuda().double().abs().sum(1) + lost(sw) * xc.cuda().double().abs().sum(1)[:, None]
+        u = ref.half_step(BF16) if out_type == BF16 else 0.0
+        mixer_ref.assert_within(got, (f * want).cpu(), (f * (err * (1 + u) + u * want.abs())).cpu(), "scaled")
+
+
+@pytest.mark.parametrize("rows,n_out", [(3, 64), (64, 9000), (200, 9024), (700, 9024), (2000, 4128)])
+@pytest.mark.parametrize("out_type", [F32, BF16])
+def test_not_a_number_scales(rs, rows, n_out, out_type):
+    x, w, _, _ = _operands(MX, rows, n_out, 96, 13)
+    clean = rs.linear(_cuda(x), _cuda(w), out_dtype=out_type)
+    xc, wc = _cuda(x), _cuda(w)
+    xc[1].view(torch.uint8)[2, 1] = 255
+    wc[1].view(torch.uint8)[5, 2] = 255
+    got = rs.linear(xc, wc, out_dtype=out_type)
+    assert bool(torch.isnan(got[2]).all()) and bool(torch.isnan(got[:, 5]).all())
+    got[2], got[:, 5] = clean[2], clean[:, 5]
+    assert _same(got, clean)
+
+
 def test_scales_at_any_address(rs):
     """MX scales that start between multiples of 4 bytes: the same values, by another kernel."""
     x, w, xv, wv = _operands(MX, 50, 100, 96, 12)
