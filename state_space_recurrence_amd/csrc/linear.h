@@ -25,9 +25,6 @@ struct LinearParams {
     int res_bf16;
 };
 
-// Rows and columns of the widest tile that one workgroup takes.
-constexpr int kLinearTile = 256;
-
 hipError_t launch_linear(const LinearParams &p, bool mx, hipStream_t s);
 
 }  // namespace rssm
