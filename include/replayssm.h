@@ -529,7 +529,7 @@ typedef struct rssm_linear_io {
  * largest of up to 16 neighbouring ones, far below the output's own rounding.
  * The order of a sum depends on the sizes, not on the row: rows of one call with
  * equal inputs get equal outputs.  Rows that start at multiples of 16 bytes (and
- * scales at one of 4) take the fast kernels; others are slower by about half.
+ * scales at one of 4) take the fast kernels; others take 2 to 3 times as long.
  */
 int replayssm_linear(const rssm_linear_desc *desc, const rssm_linear_io *io, hipStream_t stream);
 
