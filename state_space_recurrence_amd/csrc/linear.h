@@ -25,6 +25,7 @@ struct LinearParams {
     int res_bf16;
 };
 
-hipError_t launch_linear(const LinearParams &p, bool mx, hipStream_t s);
+// fast: MX operands may be multiplied by the scaled 8-bit products.
+hipError_t launch_linear(const LinearParams &p, bool mx, bool fast, hipStream_t s);
 
 }  // namespace rssm

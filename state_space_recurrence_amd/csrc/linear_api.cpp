@@ -111,6 +111,8 @@ int replayssm_linear(const rssm_linear_desc *desc, const rssm_linear_io *io, hip
         return fail(RSSM_E_UNSUPPORTED, "linear: res_dtype %d: NONE, F32 or BF16", d.res_dtype);
     if (d.activation < RSSM_ACT_NONE || d.activation > RSSM_ACT_RELU2)
         return fail(RSSM_E_ARG, "linear: activation %d is none of rssm_activation", d.activation);
+    if (d.products != RSSM_PRODUCTS_EXACT && d.products != RSSM_PRODUCTS_FAST)
+        return fail(RSSM_E_ARG, "linear: products %d is none of rssm_products", d.products);
     const bool mx = d.in_dtype == RSSM_FP8_E4M3, mx_out = d.out_dtype == RSSM_FP8_E4M3, res = d.res_dtype != RSSM_NONE;
     if (mx && d.n_in % kBlock != 0) return fail(RSSM_E_ARG, "linear: MX operands need n_in %d a multiple of 32", d.n_in);
     if (mx_out && d.n_out % kBlock != 0)
@@ -150,7 +152,7 @@ int replayssm_linear(const rssm_linear_desc *desc, const rssm_linear_io *io, hip
     p.act = d.activation;
     p.out_type = d.out_dtype;
     p.res_bf16 = d.res_dtype == RSSM_BF16;
-    return hip_status(rssm::launch_linear(p, mx, stream), "linear launch");
+    return hip_status(rssm::launch_linear(p, mx, d.products == RSSM_PRODUCTS_FAST, stream), "linear launch");
 }
 
 }  // extern "C"

@@ -9,13 +9,15 @@
 // at place c ^ (r >> 1 & 7): the 16 lanes that read at a time then touch all 64
 // banks (with r & 7 half of them: a third of the LDS cycles were conflicts).
 //
-// MX operands are multiplied in one of two ways.  Scaled 8-bit products (two
-// 32x32x64 per tile and step) run at twice the bf16 rate, but the matrix units
-// cut each product 13 binary places below the largest of those that they add at
-// once.  bf16 outputs then differ from the rounded sums of exact products by
-// 2.9e-4 of their norm (256 rows of 14432 outputs, K 4096), where the rounding
-// itself takes 1.7e-3.  fp32 and MX outputs are made of operands widened to bf16,
-// which is exact, so their sums are those of bf16 rows.  Sums are fp32.
+// MX operands are multiplied in one of two ways; sums are fp32 in both.  Widened
+// to bf16, which is exact, their sums are those of bf16 rows.  Scaled 8-bit
+// products (two 32x32x64 per tile and step) run at twice the rate, but the matrix
+// units cut each product 13 binary places below the largest of those that they
+// add at once: sums are off by 2.9e-4 of their norm (256 rows of 14432 outputs, K
+// 4096), a sixth of what rounding to bf16 takes (1.7e-3), and where large products
+// cancel, what is left of the small ones may be anything below that cut.  So these
+// are taken where the caller asks for them, and by the tiles from 64 x 64 on,
+// which are the ones that they make faster.
 //
 // What bounds it (M rows, 14432 outputs of 4096 inputs unless said otherwise):
 //   - one row: the weights' bytes; 23 us for 118 MB of bf16, 5.1 TB/s.
@@ -143,7 +145,7 @@ __device__ __forceinline__ b8v widen_codes(const u4v &c, int half, uint32_t scal
 enum Product {
     BF16,       // bf16 rows
     MX_EXACT,   // MX rows, widened to bf16: products and sums as for bf16 rows
-    MX_FAST     // MX rows, scaled 8-bit products at twice the rate
+    MX_FAST     // MX rows, scaled 8-bit products at twice the rate (few rows: as MX_EXACT)
 };
 
 // One step of a wave's TM x TN tiles of 32 x 32.
@@ -854,7 +856,7 @@ bool multiple(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p)
 
 }  // namespace
 
-hipError_t launch_linear(const LinearParams &p, bool mx, hipStream_t s) {
+hipError_t launch_linear(const LinearParams &p, bool mx, bool fast, hipStream_t s) {
     // Rows at aligned addresses are loaded straight to LDS or operands.
     const bool direct = p.w_pitch % 16 == 0 && p.x_pitch % 16 == 0 && multiple(p.x, 16) && multiple(p.w, 16) &&
                         (!mx || (multiple(p.x_scales, 4) && multiple(p.w_scales, 4)));
@@ -866,7 +868,7 @@ hipError_t launch_linear(const LinearParams &p, bool mx, hipStream_t s) {
         launch_direct<BF16, true>(p, s);
     } else {
         const bool whole = p.k_bytes % (4 * kStep) == 0;
-        if (p.out_type == RSSM_BF16) whole ? launch_direct<MX_FAST, true>(p, s) : launch_direct<MX_FAST, false>(p, s);
+        if (fast) whole ? launch_direct<MX_FAST, true>(p, s) : launch_direct<MX_FAST, false>(p, s);
         else whole ? launch_direct<MX_EXACT, true>(p, s) : launch_direct<MX_EXACT, false>(p, s);
     }
     return hipGetLastError();

@@ -27,7 +27,7 @@ _OUT_TYPES = {torch.float32: F32, torch.bfloat16: BF16, _E4M3: FP8_E4M3}
 
 class RssmLinearDesc(ctypes.Structure):
     _fields_ = [("rows", _i64)] + [(n, _i32) for n in ("n_in", "n_out", "in_dtype", "out_dtype", "res_dtype",
-                                                       "activation")] + [("scale", _f32)]
+                                                       "activation")] + [("scale", _f32), ("products", _i32)]
 
 
 class RssmLinearIO(ctypes.Structure):
@@ -178,7 +178,7 @@ def add_norm_mx(x, residual, weight, *, scale: float = 1.0, post_weight=None, ep
 
 
 def linear(x, weight, bias=None, *, activation: str | None = None, residual=None, scale: float = 1.0, out=None,
-           out_dtype: torch.dtype = torch.bfloat16, stream=None):
+           out_dtype: torch.dtype = torch.bfloat16, fast_products: bool = False, stream=None):
     """Matrix product with its epilogue (replayssm_linear):
     ``residual + scale * act(x @ weight.T + bias)``.
 
@@ -186,7 +186,11 @@ def linear(x, weight, bias=None, *, activation: str | None = None, residual=None
     or dense), or both MX pairs; bias [n_out] fp32; activation None, "silu",
     "gelu" or "relu2"; residual [rows,n_out] fp32 or bf16, which may be ``out``.
     Returns [rows,n_out] in ``out_dtype`` (of ``out`` when it is given): bf16, fp32,
-    or ``torch.float8_e4m3fn`` for an MX pair."""
+    or ``torch.float8_e4m3fn`` for an MX pair.
+
+    ``fast_products`` allows products of MX rows that may be off by 2^-13 of the
+    largest among 16 neighbouring ones (RSSM_PRODUCTS_FAST), at up to twice the
+    rate; large products that cancel may then take small ones with them."""
     act = _ACTIVATIONS.get(activation)
     if act is None:
         raise ReplaySSMError(f"activation must be None, 'silu', 'gelu' or 'relu2', got {activation!r}")
@@ -230,7 +234,7 @@ def linear(x, weight, bias=None, *, activation: str | None = None, residual=None
         if out is None:
             out = _empty((rows, n_out), out_dtype, xs.device, stream)
         op, osp = _at(out, (rows, n_out), out_dtype, dev, "out"), None
-    d = RssmLinearDesc(rows, n_in, n_out, ty, ot, rt, act, scale)
+    d = RssmLinearDesc(rows, n_in, n_out, ty, ot, rt, act, scale, 1 if fast_products else 0)
     io = RssmLinearIO(xp, pitch, xsp, wp, wsp, bp, rp, op, osp)
     rc = _lib().replayssm_linear(ctypes.addressof(d), ctypes.addressof(io), _raw_stream(stream, xs))
     if rc:
