@@ -96,6 +96,14 @@ __device__ __forceinline__ void put8(const LinearParams &p, int64_t m, int n, in
     }
 }
 
+// What the wave's lanes stored to LDS before can be read by its other lanes
+// behind, and what they read before can be overwritten.  Every lane gets here.
+__device__ __forceinline__ void wave_exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // A wave's sums of 32 TN outputs (from n0, some of them in the row) x 32 rows
 // (from m0, some of them there), through 4 TN KB of LDS of its own so that a row
 // is stored (and its residual loaded) in one piece.  16 bytes c of row r lie at
@@ -110,16 +118,18 @@ __device__ __forceinline__ void finish(const LinearParams &p, int64_t m0, int n0
         for (int g = 0; g < 4; ++g)
             *reinterpret_cast<f4v *>(lds + r * kPitch + (((8 * i + 2 * g + h) ^ (r & 7)) << 4)) =
                 f4v{acc[i][4 * g], acc[i][4 * g + 1], acc[i][4 * g + 2], acc[i][4 * g + 3]};
-    const int c = lane % kAcross, n = n0 + 8 * c, left = p.n_out - n;
-    if (left <= 0) return;   // (all four lanes of a block)
+    wave_exchange();
+    const int c = lane % kAcross, n = n0 + 8 * c, left = p.n_out - n;   // (1 or more for all four lanes of a block, or none)
     f8v bias = (f8v)0.f;
     if (p.bias) bias = load_part<false>(p.bias + n, left);
-    for (int row = lane / kAcross; row < 32; row += 64 / kAcross) {
-        if (m0 + row >= p.rows) break;
-        const f4v a = *reinterpret_cast<const f4v *>(lds + row * kPitch + (((2 * c) ^ (row & 7)) << 4));
-        const f4v b = *reinterpret_cast<const f4v *>(lds + row * kPitch + (((2 * c + 1) ^ (row & 7)) << 4));
-        put8(p, m0 + row, n, left, f8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, bias);
-    }
+#pragma unroll 1
+    for (int row = lane / kAcross; row < 32; row += 64 / kAcross)
+        if (left > 0 && m0 + row < p.rows) {
+            const f4v a = *reinterpret_cast<const f4v *>(lds + row * kPitch + (((2 * c) ^ (row & 7)) << 4));
+            const f4v b = *reinterpret_cast<const f4v *>(lds + row * kPitch + (((2 * c + 1) ^ (row & 7)) << 4));
+            put8(p, m0 + row, n, left, f8v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, bias);
+        }
+    wave_exchange();
 }
 
 // ---------------------------------------------------------------- products --
