@@ -470,6 +470,13 @@ int replayssm_add_norm(int64_t rows, int32_t dim, const void *x, int32_t x_dtype
  * values lie in fp32's range; values beyond it (scale bytes over 246) may count
  * as infinities, and of values below 2^-126 what lies under 2^-133 may be lost
  * (the last bits of codes below 2^-3 with scale bytes 0..2).
+ *
+ * What these calls write overlaps nothing else that they are given, but for a
+ * residual and its sum: residual_out of add_norm_mx may be residual, or x where
+ * the types agree, and out of replayssm_linear may be residual where the types
+ * agree.  Other overlaps are refused.  Aligned dwords that hold scales of the
+ * operands are read whole, so up to 3 bytes beside a tensor of scales are read
+ * with it (and not used).
  * ------------------------------------------------------------------------ */
 
 /* Rows to MX: x [rows, dim] at x_pitch elements per row, F32 or BF16. */

@@ -44,6 +44,39 @@ int check_codes(const char *what, const void *codes, const void *scales) {
     return RSSM_OK;
 }
 
+// Whether `bytes` bytes at `out` touch any of `rows` rows of `row` bytes that lie `pitch` apart (none for NULL).
+bool touches(const void *in, int64_t rows, int64_t row, int64_t pitch, const void *out, int64_t bytes) {
+    if (!in || !out) return false;
+    const __int128 at = (__int128) reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(in);
+    if (at + bytes <= 0 || at >= (__int128)(rows - 1) * pitch + row) return false;
+    if (at < 0) return true;
+    const int64_t in_row = (int64_t)(at % pitch);
+    return in_row < row || in_row + bytes > pitch;   // in a row, or between two and into the next
+}
+
+bool touches(const void *in, int64_t size, const void *out, int64_t bytes) { return touches(in, 1, size, size, out, bytes); }
+
+int64_t size_of(int32_t t) { return t == RSSM_F32 ? 4 : t == RSSM_BF16 ? 2 : 1; }
+
+// What a call writes: up to two buffers (rows in 8 bits: codes and scales).  Other workgroups read the operands while
+// they are written.
+struct Written {
+    const void *a;
+    int64_t a_bytes;
+    const void *b;
+    int64_t b_bytes;
+    Written(const void *out, int64_t bytes) : a(out), a_bytes(bytes), b(nullptr), b_bytes(0) {}
+    Written(const void *codes, const void *scales, int64_t rows, int64_t dim)
+        : a(codes), a_bytes(rows * dim), b(scales), b_bytes(rows * dim / kBlock) {}
+    bool over(const void *in, int64_t rows, int64_t row, int64_t pitch) const {
+        return touches(in, rows, row, pitch, a, a_bytes) || (b && touches(in, rows, row, pitch, b, b_bytes));
+    }
+    bool over(const void *in, int64_t size) const { return over(in, 1, size, size); }
+    bool over_itself() const { return b && touches(a, a_bytes, b, b_bytes); }
+};
+
+int overlap(const char *what) { return fail(RSSM_E_ARG, "%s: an output overlaps another buffer of the call", what); }
+
 }  // namespace
 
 extern "C" {
@@ -58,6 +91,9 @@ int replayssm_quantize_mx(int64_t rows, int32_t dim, const void *x, int32_t x_dt
     if (x_pitch < dim) return fail(RSSM_E_ARG, "quantize_mx: x_pitch shorter than a row");
     if (rows * (dim / 8) > (int64_t)1 << 38)   // 2^30 threads along the first axis, below 2^16 workgroups along the second
         return fail(RSSM_E_CAPACITY, "quantize_mx: more work than a launch holds");
+    const Written out(codes, scales, rows, dim);
+    const int64_t size = size_of(x_dtype);
+    if (out.over_itself() || out.over(x, rows, dim * size, x_pitch * size)) return overlap("quantize_mx");
     rssm::QuantizeParams p{x, static_cast<uint8_t *>(codes), scales, x_pitch, rows, dim};
     return hip_status(rssm::launch_quantize(p, x_dtype == RSSM_BF16, stream), "quantize launch");
 }
@@ -75,6 +111,11 @@ int replayssm_gated_norm_mx(int64_t rows, int32_t dim, int32_t groups, const voi
     if (!y || !z || !weight) return fail(RSSM_E_ARG, "gated_norm_mx: a pointer is NULL");
     RSSM_TRY(check_codes("gated_norm_mx", codes, scales));
     if (z_pitch < dim) return fail(RSSM_E_ARG, "gated_norm_mx: z_pitch shorter than a row");
+    const Written out(codes, scales, rows, dim);
+    const int64_t z_size = size_of(z_dtype);
+    if (out.over_itself() || out.over(y, rows * dim * size_of(y_dtype)) || out.over(weight, dim * 4) ||
+        out.over(z, rows, dim * z_size, z_pitch * z_size))
+        return overlap("gated_norm_mx");
     rssm::GatedNormParams p{y, z, codes, weight, z_pitch, rows, dim, groups, eps, norm_before_gate, scales};
     return hip_status(rssm::launch_gated_norm_mx(p, y_dtype == RSSM_BF16, z_dtype == RSSM_BF16, stream),
                       "gated norm launch");
@@ -92,6 +133,14 @@ int replayssm_add_norm_mx(int64_t rows, int32_t dim, const void *x, int32_t x_dt
     if (x ? !residual_out : (residual_out || post_weight))
         return fail(RSSM_E_ARG, "add_norm_mx: residual_out goes with x, and post_weight needs it");
     RSSM_TRY(check_codes("add_norm_mx", codes, scales));
+    const Written out(codes, scales, rows, dim);
+    const int64_t x_bytes = rows * dim * size_of(x_dtype), res_bytes = rows * dim * size_of(res_dtype);
+    const Written sum(residual_out, residual_out ? res_bytes : 0);   // a row is read whole before it is written
+    if (out.over_itself() || out.over(x, x_bytes) || out.over(residual, res_bytes) || out.over(residual_out, res_bytes) ||
+        out.over(weight, dim * 4) || out.over(post_weight, dim * 4) || sum.over(weight, dim * 4) ||
+        sum.over(post_weight, dim * 4) || (residual_out != residual && sum.over(residual, res_bytes)) ||
+        ((residual_out != x || x_dtype != res_dtype) && sum.over(x, x_bytes)))
+        return overlap("add_norm_mx");
     rssm::AddNormParams p{x, residual, residual_out, codes, weight, post_weight, rows, dim, scale, eps, scales};
     return hip_status(rssm::launch_add_norm_mx(p, x && x_dtype == RSSM_BF16, res_dtype == RSSM_BF16, stream),
                       "add norm launch");
@@ -134,6 +183,14 @@ int replayssm_linear(const rssm_linear_desc *desc, const rssm_linear_io *io, hip
         return fail(RSSM_E_ARG, "linear: x_pitch shorter than a row, or MX rows that are not dense");
     if (io->x_pitch > (int64_t)1 << 22)   // a tile's rows are addressed in 31 bits
         return fail(RSSM_E_CAPACITY, "linear: x_pitch over 2^22 elements");
+    const int64_t k_bytes = (int64_t)d.n_in * size;
+    const int64_t out_size = size_of(d.out_dtype);
+    const Written out = mx_out ? Written(io->out, io->out_scales, d.rows, d.n_out) : Written(io->out, d.rows * d.n_out * out_size);
+    if (out.over_itself() || out.over(io->x, d.rows, k_bytes, io->x_pitch * size) || out.over(io->weight, d.n_out * k_bytes) ||
+        out.over(io->bias, (int64_t)d.n_out * 4) ||
+        (mx && (out.over(io->x_scales, d.rows * d.n_in / kBlock) || out.over(io->weight_scales, (int64_t)d.n_out * d.n_in / kBlock))) ||
+        ((io->residual != io->out || d.res_dtype != d.out_dtype) && out.over(io->residual, d.rows * d.n_out * size_of(d.res_dtype))))
+        return overlap("linear");
     rssm::LinearParams p{};
     p.x = io->x;
     p.w = io->weight;
