@@ -44,13 +44,15 @@ int check_codes(const char *what, const void *codes, const void *scales) {
     return RSSM_OK;
 }
 
+typedef __int128 wide;   // any pitch in bytes
+
 // Whether `bytes` bytes at `out` touch any of `rows` rows of `row` bytes that lie `pitch` apart (none for NULL).
-bool touches(const void *in, int64_t rows, int64_t row, int64_t pitch, const void *out, int64_t bytes) {
+bool touches(const void *in, int64_t rows, int64_t row, wide pitch, const void *out, int64_t bytes) {
     if (!in || !out) return false;
-    const __int128 at = (__int128) reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(in);
-    if (at + bytes <= 0 || at >= (__int128)(rows - 1) * pitch + row) return false;
+    const wide at = (wide) reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(in);
+    if (at + bytes <= 0 || at >= (rows - 1) * pitch + row) return false;
     if (at < 0) return true;
-    const int64_t in_row = (int64_t)(at % pitch);
+    const wide in_row = at % pitch;
     return in_row < row || in_row + bytes > pitch;   // in a row, or between two and into the next
 }
 
@@ -68,7 +70,7 @@ struct Written {
     Written(const void *out, int64_t bytes) : a(out), a_bytes(bytes), b(nullptr), b_bytes(0) {}
     Written(const void *codes, const void *scales, int64_t rows, int64_t dim)
         : a(codes), a_bytes(rows * dim), b(scales), b_bytes(rows * dim / kBlock) {}
-    bool over(const void *in, int64_t rows, int64_t row, int64_t pitch) const {
+    bool over(const void *in, int64_t rows, int64_t row, wide pitch) const {
         return touches(in, rows, row, pitch, a, a_bytes) || (b && touches(in, rows, row, pitch, b, b_bytes));
     }
     bool over(const void *in, int64_t size) const { return over(in, 1, size, size); }
@@ -93,7 +95,7 @@ int replayssm_quantize_mx(int64_t rows, int32_t dim, const void *x, int32_t x_dt
         return fail(RSSM_E_CAPACITY, "quantize_mx: more work than a launch holds");
     const Written out(codes, scales, rows, dim);
     const int64_t size = size_of(x_dtype);
-    if (out.over_itself() || out.over(x, rows, dim * size, x_pitch * size)) return overlap("quantize_mx");
+    if (out.over_itself() || out.over(x, rows, dim * size, (wide)x_pitch * size)) return overlap("quantize_mx");
     rssm::QuantizeParams p{x, static_cast<uint8_t *>(codes), scales, x_pitch, rows, dim};
     return hip_status(rssm::launch_quantize(p, x_dtype == RSSM_BF16, stream), "quantize launch");
 }
@@ -114,7 +116,7 @@ int replayssm_gated_norm_mx(int64_t rows, int32_t dim, int32_t groups, const voi
     const Written out(codes, scales, rows, dim);
     const int64_t z_size = size_of(z_dtype);
     if (out.over_itself() || out.over(y, rows * dim * size_of(y_dtype)) || out.over(weight, dim * 4) ||
-        out.over(z, rows, dim * z_size, z_pitch * z_size))
+        out.over(z, rows, dim * z_size, (wide)z_pitch * z_size))
         return overlap("gated_norm_mx");
     rssm::GatedNormParams p{y, z, codes, weight, z_pitch, rows, dim, groups, eps, norm_before_gate, scales};
     return hip_status(rssm::launch_gated_norm_mx(p, y_dtype == RSSM_BF16, z_dtype == RSSM_BF16, stream),

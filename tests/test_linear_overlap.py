@@ -77,3 +77,11 @@ def test_calls_without_rows_overlap_nothing(m):  # noqa: F811
     L = m._lib()
     assert L.replayssm_quantize_mx(0, 64, FAR, 1, 64, FAR, FAR, None) == 0
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_pitches_that_64_bits_hold_only_as_elements(m):  # noqa: F811
+    """Their bytes between rows are more than 2^63."""
+    L = m._lib()
+    for pitch in (1 << 62, (1 << 62) + 16, (1 << 63) - 1):
+        _refused(m, L.replayssm_quantize_mx(4, 64, FAR, 0, pitch, FAR, 2 * FAR, None))
+        _refused(m, L.replayssm_gated_norm_mx(4, 64, 1, FAR, 0, 2 * FAR, 0, pitch, 3 * FAR, 1e-5, 0, 2 * FAR, 4 * FAR, None))
