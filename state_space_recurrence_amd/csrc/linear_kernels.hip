@@ -19,16 +19,21 @@
 // are taken where the caller asks for them, and by the tiles from 64 x 64 on,
 // which are the ones that they make faster.
 //
-// What bounds it (M rows, 14432 outputs of 4096 inputs unless said otherwise):
-//   - one row: the weights' bytes; 23 us for 118 MB of bf16, 5.1 TB/s.
-//   - tens of rows: loads in flight.  A compute unit keeps about 110 of its L1's
-//     requests (128 bytes) on their way; 64 rows take 27 us in bf16, 18 in MX.
-//   - hundreds: the same: 256 rows 47 us in bf16, 30 in MX.
-//   - thousands: power.  The clock falls to 1.6 GHz (bf16) or 1.7 (MX), with the
-//     matrix units busy 81 % and 73 % of its cycles: 8192^3 takes 865 us (1.27
-//     PFLOP/s) and 475 us (2.3).  With all loads from L2 they are busy 98 % and the
-//     clock falls to 1.4: 834 us.  Tiles that stay with a workgroup, the next one's
-//     loads behind the stores of the last, measured the same and were dropped.
+// What bounds it (rows of 4096 inputs and 14432 outputs unless said otherwise; MX
+// by exact products, by fast ones in parentheses):
+//   - one row: the weights' bytes in bf16, 23 us for 118 MB, 5.1 TB/s.  In MX 20 us
+//     (14) for 61 MB: a SIMD has one wave, which reads, widens and multiplies a
+//     step after the other.
+//   - tens of rows: 64 take 26 us in bf16, 20 in MX (15), for the same reasons.
+//   - hundreds: 256 rows 46 us in bf16, 39 in MX (25).  In bf16 loads in flight: a
+//     compute unit has about 120 of its L1's requests (128 bytes) on their way at
+//     any time.  In MX the widening: the vector units issue in half of the cycles,
+//     the matrix units work in 40 %, and a wave does one after the other.
+//   - thousands: the matrix units, at the clock that their work leaves.  8192^3
+//     takes 881 us (1.25 PFLOP/s) in bf16 and 769 (482) in MX, the matrix units busy
+//     71 %, 80 % (57 %) of the cycles at 1.7, 1.8 (2.0) GHz.  That is no bound yet: a
+//     library's bf16 product takes 691 us.  Tiles that stay with a workgroup, the next
+//     one's loads behind the stores of the last, measured the same and were dropped.
 #include "linear.h"
 
 #include "mixer_device.h"
@@ -224,8 +229,8 @@ __device__ __forceinline__ void read_chunks(operand &o, const char *tile, int la
 
 // Tiles of 64 outputs x 64 rows, staged through registers: a row may start at
 // any element and end at any.  Four waves of 32 x 32.  16, 256 and 2048 rows take
-// 2.2, 2.6 and 2.8 times the aligned kernels' time (4095 inputs, 14432 outputs: 58 us
-// where 4096 take 26; 125, 47; 6143 inputs, 4096 outputs: 294, 6144: 105).
+// 2.4, 2.6 and 2.7 times the aligned kernels' time (4095 inputs, 14432 outputs: 57 us
+// where 4096 take 23; 122, 46; 6143 inputs, 4096 outputs: 257, 6144: 97).
 template <bool MX>
 __global__ void __launch_bounds__(256) linear_any_kernel(LinearParams p) {
     constexpr int B = 64;
